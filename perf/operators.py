@@ -165,9 +165,6 @@ def prepare(case, seed):
         if op == "norm_bwd":
             st["wsb"] = stp.staple_norm_workspace_bytes(T, case["D"])
             st["ws"] = torch.zeros(max(st["wsb"], 1), dtype=torch.uint8, device="cuda")
-        if op == "matmul_i8":
-            st["wsb"] = stp.staple_matmul_i8_workspace_bytes(T, case["N"], case["K"])
-            st["ws"] = torch.zeros(max(st["wsb"], 1), dtype=torch.uint8, device="cuda")
     return st
 
 
@@ -215,7 +212,7 @@ def _run_own(st):
         stp.staple_quant_rows(st["ctx"], st["dt"], T, case["D"], st["x"], st["q"], st["scale"])
         return st["q"], st["scale"]
     stp.staple_matmul_i8(st["ctx"], st["dt"], T, case["N"], case["K"], st["a"], st["a_scale"],
-                         st["b"], st["b_scale"], st["y"], st["ws"], st["wsb"])
+                         st["b"], st["b_scale"], st["y"])
     return st["y"]
 
 
