@@ -406,6 +406,110 @@ staple_status staple_ffn_bwd(staple_context* ctx, staple_dtype dtype, int32_t T,
                              float* dw_gate, float* dw_up, float* dw_down, void* workspace,
                              size_t workspace_bytes, staple_stream stream);
 
+/* ----------------------------------- around the layer: norm and dropout */
+
+/* The residual add, dropout and norm that stand between one layer and the
+ * next in a transformer block:
+ *     s = residual + dropout(x),   y = (s - mean) rstd w + b
+ * and their backward pass.  dtype is the type of every [T][D] tensor and of
+ * weight and bias; arithmetic, sums, mean and rstd are fp32.  D is at most
+ * 16384 (STAPLE_EUNSUPPORTED beyond) and need not be a multiple of anything;
+ * pointers need only their element's alignment.  (Rows of a multiple of 8
+ * elements on 16-byte aligned pointers take the vector path.)  T may be 0.
+ * The tensors of one call must not overlap, except where "may be" says that
+ * an output is allowed the very address of an input. */
+typedef enum staple_norm {
+  STAPLE_NORM_LAYER = 0, /* LayerNorm: mean and variance of the row */
+  STAPLE_NORM_RMS = 1    /* RMSNorm: mean = 0 */
+} staple_norm;
+
+/* Dropout whose mask is never stored: element (t, d) is dropped when its
+ * 16-bit draw is below round(p * 65536), else multiplied by the inverse of
+ * the probability of being kept (so p counts to the nearest 2^-16, and p = 1
+ * drops everything).  The draws come from Philox4x32-10 (Salmon et al., SC
+ * 2011): key = rng[0]; counter = (t * ceil(D / 8) + d / 8) in the low 64 bits
+ * and rng[1] + site in the high 64; element d % 8 = i takes the low (even i)
+ * or high (odd i) half of output word i / 2.  The mask thus depends on rng,
+ * site, D and the position alone, and the backward pass draws it again.
+ *   p      in [0, 1]; round(p * 65536) = 0 is no dropout (rng is not read)
+ *   site   tells apart the dropouts of one step: give each its own
+ *   rng    device, {seed, offset}, 8-byte aligned; read by the kernels, so a
+ *          captured graph takes new values at every replay.  Advance the
+ *          offset by the number of sites after each step. */
+typedef struct staple_drop {
+  double p;
+  uint64_t site;
+  const uint64_t* rng;
+} staple_drop;
+
+/* Forward.
+ *   x          [T][D]
+ *   residual   [T][D], or NULL (s = dropout(x))
+ *   drop       NULL: no dropout
+ *   weight, bias   [D], or NULL (1 and 0)
+ *   eps        >= 0, added to the variance
+ *   sum        out [T][D]: s, rounded to dtype; the norm is taken of the
+ *              rounded sum, which the backward pass reads.  May be x or
+ *              residual.  Required with residual or drop (EINVAL); else
+ *              NULL (s = x) or a copy of x
+ *   y          out [T][D]; may be x or residual
+ *   mean, rstd out fp32 [T], or NULL; what the backward pass needs
+ * Nothing else is kept.  One launch. */
+staple_status staple_norm_fwd(staple_context* ctx, staple_dtype dtype, staple_norm kind, int32_t T,
+                              int32_t D, const void* x, const void* residual,
+                              const staple_drop* drop, const void* weight, const void* bias,
+                              float eps, void* sum, void* y, float* mean, float* rstd,
+                              staple_stream stream);
+
+/* Device scratch of staple_norm_bwd for T rows of D (0 for a bad size).  No
+ * initial contents are needed; one call at a time per workspace. */
+size_t staple_norm_workspace_bytes(int32_t T, int32_t D);
+
+/* Backward:
+ *   ds = rstd (dy w - mean(dy w) [LayerNorm] - xhat mean(dy w xhat)) + dsum_in
+ *   dx = dropout(ds) with the forward's mask,  xhat = (s - mean) rstd
+ *   dw[d] = sum_t dy xhat,  db[d] = sum_t dy        (fp32, written, not added)
+ *   dy         [T][D] gradient of y
+ *   s          [T][D]: the forward's sum (its x if it had none)
+ *   weight     [D] or NULL, as in the forward
+ *   mean, rstd fp32 [T] of the forward (mean is not read for RMSNorm)
+ *   dsum_in    [T][D] gradient that reaches s along the residual, or NULL
+ *   drop       the forward's, or NULL
+ *   dsum       out [T][D]: ds, the residual's gradient; NULL: not wanted
+ *   dx         out [T][D]; NULL: not wanted (without dropout it equals dsum)
+ *   dw, db     out fp32 [D]; NULL: not wanted
+ *   workspace  staple_norm_workspace_bytes(T, D), 16-byte aligned; NULL is
+ *              allowed when dw and db are
+ * dsum and dx may each be dy, s or dsum_in.  The sums over T are taken in an
+ * order that depends on the sizes alone.  One launch, and a small one for dw
+ * and db. */
+staple_status staple_norm_bwd(staple_context* ctx, staple_dtype dtype, staple_norm kind, int32_t T,
+                              int32_t D, const void* dy, const void* s, const void* weight,
+                              const float* mean, const float* rstd, const void* dsum_in,
+                              const staple_drop* drop, void* dsum, void* dx, float* dw, float* db,
+                              void* workspace, size_t workspace_bytes, staple_stream stream);
+
+/* out = residual + dropout(x), any D.  residual may be NULL: with the
+ * forward's drop this is also dropout's backward pass (dx = dropout(dout)).
+ * out may be x or residual. */
+staple_status staple_dropout(staple_context* ctx, staple_dtype dtype, int32_t T, int32_t D,
+                             const void* x, const void* residual, const staple_drop* drop,
+                             void* out, staple_stream stream);
+
+/* --------------------------------------------------------- 8-bit products */
+
+/* Rows quantised to 8-bit integers: scale[t] = fp32(max_d |x[t][d]| / 127),
+ * q[t][d] = x[t][d] / scale[t] rounded to the nearest integer, ties to even
+ * (the exact quotient is rounded), within [-127, 127].  A row of zeros has
+ * scale 0 and q 0.  A row that holds an infinity or a NaN has that as its
+ * scale (NaN before infinity) and q 0, so products with it are NaN.
+ *   x   [T][D] (dtype), D at most 32768 (STAPLE_EUNSUPPORTED beyond)
+ *   q   out int8 [T][D];  scale  out fp32 [T]
+ * The same call quantises a weight [out][in] with one scale per output
+ * channel. */
+staple_status staple_quant_rows(staple_context* ctx, staple_dtype dtype, int32_t T, int32_t D,
+                                const void* x, int8_t* q, float* scale, staple_stream stream);
+
 /* ------------------------------------------------ host optimizer (AdamW) */
 
 typedef struct staple_adamw {

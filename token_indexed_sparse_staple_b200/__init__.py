@@ -15,7 +15,7 @@ import ctypes as C
 import numpy as np
 
 from . import _lib
-from ._lib import staple_adamw, staple_embed
+from ._lib import staple_adamw, staple_drop, staple_embed
 
 STAPLE_OK = 0
 STAPLE_EINVAL, STAPLE_EIDRANGE, STAPLE_ECUDA, STAPLE_ENOMEM = -1, -2, -3, -4
@@ -24,9 +24,10 @@ STAPLE_BF16, STAPLE_F32 = 0, 1
 STAPLE_EMBED_NONE, STAPLE_EMBED_TABLE, STAPLE_EMBED_ROWS = 0, 1, 2
 STAPLE_TABLE_DEVICE, STAPLE_TABLE_HOST_PINNED, STAPLE_TABLE_HOST_REGISTER = 1, 2, 4
 STAPLE_EMBED_REPLACE_UP = 1
+STAPLE_NORM_LAYER, STAPLE_NORM_RMS = 0, 1
 
 __all__ = [n for n in _lib.SIGNATURES] + [
-    "StapleError", "staple_embed", "staple_adamw", "make_embed", "lib",
+    "StapleError", "staple_embed", "staple_adamw", "staple_drop", "make_embed", "make_drop", "lib",
 ]
 
 
@@ -71,6 +72,13 @@ def make_embed(mode: int, base=None, row_pitch: int = 0, index=None, n_rows: int
     """flags = STAPLE_EMBED_REPLACE_UP: the STEM layer (the row replaces the
     up-projection)."""
     return staple_embed(mode, flags, _p(base), row_pitch, _p(index), n_rows)
+
+
+def make_drop(p: float, rng, site: int = 0) -> staple_drop:
+    """The dropout argument: rng is a device int64 (or uint64) tensor {seed,
+    offset}, which the caller keeps alive; site tells apart the dropouts of one
+    step (see include/staple.h)."""
+    return staple_drop(float(p), site, _p(rng))
 
 
 # ------------------------------------------------------------------ context
@@ -275,3 +283,43 @@ def staple_gather_unique_rows_bulk(ctx, cache, table, unique, U_dev, T, slot, mi
                                              _p(staging_host), _p(staging_dev), _p(list_host),
                                              chunk_rows, threads, _stream(stream)),
         "staple_gather_unique_rows_bulk")
+
+
+# ------------------------------------------------ norm, dropout, 8-bit rows
+
+def _drop(d):
+    return C.byref(d) if d is not None else None
+
+
+def staple_norm_fwd(ctx, dtype, kind, T, D, x, y, weight=None, bias=None, eps=1e-5, residual=None,
+                    drop=None, sum=None, mean=None, rstd=None, stream=None):
+    """s = residual + dropout(x); y = norm(s) (see include/staple.h)."""
+    _ok(lib().staple_norm_fwd(ctx, dtype, kind, T, D, _p(x), _p(residual), _drop(drop), _p(weight),
+                              _p(bias), eps, _p(sum), _p(y), _p(mean), _p(rstd), _stream(stream)),
+        "staple_norm_fwd")
+
+
+def staple_norm_workspace_bytes(T: int, D: int) -> int:
+    return int(lib().staple_norm_workspace_bytes(T, D))
+
+
+def staple_norm_bwd(ctx, dtype, kind, T, D, dy, s, rstd, dsum, mean=None, weight=None,
+                    dsum_in=None, drop=None, dx=None, dw=None, db=None, workspace=None,
+                    workspace_bytes=0, stream=None):
+    """Gradients of staple_norm_fwd: dsum, dx, dw and db (see include/staple.h)."""
+    _ok(lib().staple_norm_bwd(ctx, dtype, kind, T, D, _p(dy), _p(s), _p(weight), _p(mean),
+                              _p(rstd), _p(dsum_in), _drop(drop), _p(dsum), _p(dx), _p(dw), _p(db),
+                              _p(workspace), workspace_bytes, _stream(stream)), "staple_norm_bwd")
+
+
+def staple_dropout(ctx, dtype, T, D, x, drop, out, residual=None, stream=None):
+    """out = residual + dropout(x); with the forward's drop and no residual,
+    dropout's backward pass (see include/staple.h)."""
+    _ok(lib().staple_dropout(ctx, dtype, T, D, _p(x), _p(residual), _drop(drop), _p(out),
+                             _stream(stream)), "staple_dropout")
+
+
+def staple_quant_rows(ctx, dtype, T, D, x, q, scale, stream=None):
+    """Rows to 8-bit integers with one scale each (see include/staple.h)."""
+    _ok(lib().staple_quant_rows(ctx, dtype, T, D, _p(x), _p(q), _p(scale), _stream(stream)),
+        "staple_quant_rows")

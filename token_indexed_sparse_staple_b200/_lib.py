@@ -33,6 +33,10 @@ class staple_adamw(C.Structure):
                 ("weight_decay", C.c_float), ("step", i32)]
 
 
+class staple_drop(C.Structure):
+    _fields_ = [("p", C.c_double), ("site", C.c_uint64), ("rng", vp)]
+
+
 # name -> (restype, argtypes); mirrors include/staple.h
 SIGNATURES = {
     "staple_abi_version": (C.c_int, []),
@@ -71,6 +75,13 @@ SIGNATURES = {
     "staple_embed_grad": (c_status, [vp, C.c_int, i32, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp,
                                      sz, vp]),
     "staple_embed_grad_static": (c_status, [C.c_int, i32, i32, vp, i64, vp, vp, vp, vp, vp]),
+    "staple_norm_fwd": (c_status, [vp, C.c_int, C.c_int, i32, i32, vp, vp, P(staple_drop), vp, vp,
+                                   C.c_float, vp, vp, vp, vp, vp]),
+    "staple_norm_workspace_bytes": (sz, [i32, i32]),
+    "staple_norm_bwd": (c_status, [vp, C.c_int, C.c_int, i32, i32, vp, vp, vp, vp, vp, vp,
+                                   P(staple_drop), vp, vp, vp, vp, vp, sz, vp]),
+    "staple_dropout": (c_status, [vp, C.c_int, i32, i32, vp, vp, P(staple_drop), vp, vp]),
+    "staple_quant_rows": (c_status, [vp, C.c_int, i32, i32, vp, vp, vp, vp]),
 }
 
 _lib = None

@@ -112,6 +112,28 @@ staple_status tc_decode_fwd(const DeviceInfo& di, int T, int D, int F, const voi
                             void* z, void* y, void* g_save, void* h_save, void* ws,
                             int32_t* err, cudaStream_t st);
 
+// norm.cu: the norm with the residual add and dropout in front of it, and
+// dropout on its own.  D is at most kNormMaxD; the backward pass leaves the
+// partial sums of dw and db of at most kNormMaxBlocks blocks in `part`.
+constexpr int kNormMaxD = 16384;
+constexpr int kNormMaxBlocks = 640;
+size_t norm_workspace_bytes(int T, int D);
+staple_status launch_norm_fwd(bool bf16, bool rms, int T, int D, const void* x, const void* res,
+                              const staple_drop* drop, const void* w, const void* b, float eps,
+                              void* sum, void* y, float* mean, float* rstd, cudaStream_t st);
+staple_status launch_norm_bwd(const DeviceInfo& di, bool bf16, bool rms, int T, int D,
+                              const void* dy, const void* s, const void* w, const float* mean,
+                              const float* rstd, const void* dsum_in, const staple_drop* drop,
+                              void* dsum, void* dx, float* dw, float* db, float* part,
+                              cudaStream_t st);
+staple_status launch_dropout(bool bf16, int T, int D, const void* x, const void* res,
+                             const staple_drop* drop, void* out, cudaStream_t st);
+
+// quant.cu: D is at most kQuantMaxD
+constexpr int kQuantMaxD = 32768;
+staple_status launch_quant_rows(bool bf16, int T, int D, const void* x, int8_t* q, float* scale,
+                                cudaStream_t st);
+
 // simt_f32.cu (fp32 on CUDA cores)
 staple_status f32_ffn_fwd(int T, int D, int F, const float* x, const staple_embed* e,
                           const float* wg, const float* wu, const float* wd, float* z, float* y,

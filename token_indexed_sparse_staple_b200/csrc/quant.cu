@@ -1,0 +1,162 @@
+// Rows quantised to 8-bit integers with one scale each, the operands of
+// staple_matmul_i8:
+//
+//   scale = fp32(max |x| / 127),  q = x / scale rounded to nearest even
+//
+// Bound by memory: a row is read once (it stays in registers between the
+// maximum and the rounding) and its bytes written once.
+//
+// The quotient is rounded exactly, ties included, at the price of a
+// multiplication: q0 = rint(x * (1 / scale)) by adding 1.5 * 2^23, whose sum
+// holds q0 in its low byte, and the remainder r = x - q0 scale, which one fma
+// gives exactly wherever it matters (near a tie both terms are multiples of
+// 2^(e-24), for scale in [2^e, 2^(e+1)), and |r| < 2^e).  |r| < scale / 2
+// shows that q0 is the nearest integer; a group of eight with any other
+// element (a tie, or a product rounded across one) is divided in fp64, where
+// a quotient of two fp32 numbers cannot be rounded onto a half it does not
+// equal.
+#include <algorithm>
+
+#include "internal.h"
+#include "rows.cuh"
+
+namespace stp {
+
+namespace {
+
+struct QuantParams {
+  const void* x;
+  int8_t* q;
+  float* scale;
+  int32_t T, D, tpr;
+};
+
+constexpr float kRintMagic = 12582912.0f;   // 1.5 * 2^23
+// Below this maximum (2^-60) the reciprocal of the scale or the remainder
+// could leave the normal range: those rows divide in fp64.
+constexpr float kTiny = 8.67361738e-19f;
+
+__device__ __forceinline__ uint32_t q_exact(float x, double scale) {
+  double d = rint(double(x) / scale);
+  d = fmin(fmax(d, -127.0), 127.0);   // a subnormal scale may be far below max / 127
+  return uint32_t(int(d)) & 0xffu;
+}
+
+template <bool BF16, int NV, bool VEC>
+__global__ void __launch_bounds__(1024) quant_rows_kernel(const QuantParams p) {
+  __shared__ uint32_t red[32];
+  const int rpb = blockDim.x / p.tpr;
+  const int rg = threadIdx.x / p.tpr, t = threadIdx.x - rg * p.tpr;
+  const int64_t row = int64_t(blockIdx.x) * rpb + rg;
+  const bool row_ok = row < p.T;
+  const int G = (p.D + kGroup - 1) / kGroup;
+  const int64_t base = row * p.D;
+  Raw8<BF16> xr[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int g = t + i * p.tpr;
+    xr[i] = zero_raw8<BF16>();
+    if (row_ok && g < G)
+      xr[i] = load_raw8<BF16, VEC>(p.x, base + g * kGroup, min(kGroup, p.D - g * kGroup));
+  }
+  // the largest |x| as bits: a NaN is above the infinity, which is above
+  // every finite number
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(xr[i].get(j)) & 0x7fffffffu);
+  if (p.tpr >= 32) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (p.tpr > 32) {
+      const int warp = threadIdx.x >> 5, wpr = p.tpr >> 5;
+      if ((threadIdx.x & 31) == 0) red[warp] = m;
+      __syncthreads();
+      const int w0 = warp / wpr * wpr;
+      for (int j = 0; j < wpr; ++j) m = max(m, red[w0 + j]);
+    }
+  } else {
+    for (int k = p.tpr >> 1; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
+  }
+  if (!row_ok) return;
+  const float amax = __uint_as_float(m);
+  const float scale = amax / 127.0f;
+  const bool finite = m < 0x7f800000u;
+  if (t == 0) p.scale[row] = scale;
+  const float inv = 1.0f / scale, half = 0.5f * scale;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int g = t + i * p.tpr;
+    if (g >= G) break;
+    uint32_t b[8];
+    bool exact = false;
+    if (finite && amax >= kTiny) {
+      float worst = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = xr[i].get(j);
+        const float s = fmaf(x, inv, kRintMagic);
+        worst = fmaxf(worst, fabsf(fmaf(-(s - kRintMagic), scale, x)));
+        b[j] = __float_as_uint(s) & 0xffu;
+      }
+      exact = worst < half;
+    }
+    if (!exact) {
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j) {
+        float x = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k == j) x = xr[i].get(k);
+        const uint32_t v = finite && scale > 0.0f ? q_exact(x, double(scale)) : 0u;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k == j) b[k] = v;
+      }
+    }
+    int8_t* dst = p.q + base + g * kGroup;
+    const uint32_t lo = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+    const uint32_t hi = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
+    if constexpr (VEC) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+    } else {
+      const int n = min(kGroup, p.D - g * kGroup);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) dst[j] = int8_t(b[j]);
+    }
+  }
+}
+
+template <bool BF16, bool VEC>
+void go(const QuantParams& p, int nv, unsigned grid, int block, cudaStream_t st) {
+  switch (nv) {
+    case 1: quant_rows_kernel<BF16, 1, VEC><<<grid, block, 0, st>>>(p); break;
+    case 2: quant_rows_kernel<BF16, 2, VEC><<<grid, block, 0, st>>>(p); break;
+    default: quant_rows_kernel<BF16, 4, VEC><<<grid, block, 0, st>>>(p); break;
+  }
+}
+
+}  // namespace
+
+staple_status launch_quant_rows(bool bf16, int T, int D, const void* x, int8_t* q, float* scale,
+                                cudaStream_t st) {
+  if (T == 0) return STAPLE_OK;
+  QuantParams p{x, q, scale, T, D, 0};
+  const int G = groups_of(D);
+  const int nv = G <= 1024 ? 1 : (G <= 2048 ? 2 : 4);
+  p.tpr = threads_per_row(G, nv);
+  const int rpb = std::max(1, 256 / p.tpr);
+  const unsigned grid = unsigned((int64_t(T) + rpb - 1) / rpb);
+  const int block = rpb * p.tpr;
+  const bool vec = D % kGroup == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 &&
+                   (reinterpret_cast<uintptr_t>(q) & 7u) == 0;
+  STP_LAUNCH("quant_rows", st,
+             if (bf16) { if (vec) go<true, true>(p, nv, grid, block, st);
+                         else go<true, false>(p, nv, grid, block, st); }
+             else { if (vec) go<false, true>(p, nv, grid, block, st);
+                    else go<false, false>(p, nv, grid, block, st); });
+  return cudaGetLastError() == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+}
+
+}  // namespace stp

@@ -1,0 +1,197 @@
+// Row helpers of the norm, dropout and quantisation kernels: groups of eight
+// consecutive elements of a row, sums over the threads that share a row, and
+// the dropout's counter-based random numbers.
+#pragma once
+
+#include "common.cuh"
+
+namespace stp {
+
+constexpr int kGroup = 8;   // elements a thread handles together
+
+// Eight consecutive elements as they lie in memory: four 32-bit words of bf16
+// pairs, or eight fp32 words.
+template <bool BF16>
+struct Raw8 {
+  uint32_t w[BF16 ? 4 : 8];
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (BF16) return (i & 1) ? bf_hi(w[i >> 1]) : bf_lo(w[i >> 1]);
+    else return __uint_as_float(w[i]);
+  }
+};
+
+// Load n <= 8 elements from element offset `off`; the rest are zero.  VEC:
+// n == 8 and the address is 16-byte aligned.  Plain (coherent) loads: the
+// outputs of these kernels may share the inputs' memory.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ Raw8<BF16> load_raw8(const void* base, int64_t off, int n) {
+  Raw8<BF16> r;
+  if constexpr (VEC) {
+    if constexpr (BF16) {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
+      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(base) + off);
+      const uint4 a = p[0], b = p[1];
+      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+      r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+    }
+  } else if constexpr (BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + off;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = 2 * i < n ? p[2 * i] : 0u;
+      const uint32_t hi = 2 * i + 1 < n ? p[2 * i + 1] : 0u;
+      r.w[i] = lo | (hi << 16);
+    }
+  } else {
+    const uint32_t* p = static_cast<const uint32_t*>(base) + off;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = i < n ? p[i] : 0u;
+  }
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> zero_raw8() {
+  Raw8<BF16> r;
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 4 : 8); ++i) r.w[i] = 0u;
+  return r;
+}
+
+// Eight floats rounded to the element type (bf16: to nearest even, the
+// storage rounding of every bf16 tensor of the library).
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> pack_raw8(const float (&v)[8]) {
+  Raw8<BF16> r;
+  if constexpr (BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = pack_bf2(v[2 * i], v[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(v[i]);
+  }
+  return r;
+}
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store_raw8(void* base, int64_t off, int n, const Raw8<BF16>& r) {
+  if constexpr (VEC) {
+    if constexpr (BF16) {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + off) =
+          make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    } else {
+      uint4* p = reinterpret_cast<uint4*>(static_cast<uint32_t*>(base) + off);
+      p[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+      p[1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+    }
+  } else if constexpr (BF16) {
+    uint16_t* p = static_cast<uint16_t*>(base) + off;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = uint16_t((i & 1) ? r.w[i >> 1] >> 16 : r.w[i >> 1] & 0xffffu);
+  } else {
+    uint32_t* p = static_cast<uint32_t*>(base) + off;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = r.w[i];
+  }
+}
+
+// Groups of a row of D elements.
+inline int groups_of(int D) { return int((int64_t(D) + kGroup - 1) / kGroup); }
+
+// Threads per row for nv groups per thread: a power of two up to 32, else
+// whole warps.
+inline int threads_per_row(int groups, int nv) {
+  const int need = (groups + nv - 1) / nv;
+  if (need > 32) return (need + 31) / 32 * 32;
+  int t = 1;
+  while (t < need) t <<= 1;
+  return t;
+}
+
+// Threads that share a row: tpr of them, either a power of two up to 32
+// (several rows per warp) or a multiple of 32 (whole warps).  Sums of N
+// values over a row's threads, the same in each of them and in an order that
+// depends on tpr alone.  red: N * 32 floats, free for the call (a caller that
+// uses it again puts a block barrier, or another array, in between).  Every
+// thread of the block calls it.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float* red) {
+  const int width = tpr < 32 ? tpr : 32;
+  for (int m = width >> 1; m > 0; m >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
+  if (tpr <= 32) return;
+  const int warp = threadIdx.x >> 5, wpr = tpr >> 5;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[k * 32 + warp] = v[k];
+  __syncthreads();
+  const int w0 = warp / wpr * wpr;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    float s = red[k * 32 + w0];
+    for (int j = 1; j < wpr; ++j) s += red[k * 32 + w0 + j];
+    v[k] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Dropout: Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", SC 2011).  One call gives 128 bits, a 16-bit
+// draw for each element of a group of eight, so the generator costs ten rounds
+// per eight elements.  Group g of row t has the counter (t * ceil(D / 8) + g)
+// in its low 64 bits and offset + site in its high 64 bits; the key is the
+// seed.  An element is kept when its draw is >= thr = round(p * 2^16).  The
+// mask depends on nothing else: not on the kernel, its launch shape or the
+// element type, so the backward pass and every fused form draw the same one.
+// ---------------------------------------------------------------------------
+struct DropParams {
+  const uint64_t* rng;   // device {seed, offset}; NULL: no dropout
+  uint64_t site;
+  uint32_t thr;          // keep if draw >= thr (65536: keep nothing)
+  float scale;           // 65536 / (65536 - thr)
+};
+
+struct DropKey {
+  uint32_t k0, k1, c2, c3;
+};
+
+__device__ __forceinline__ DropKey drop_key(const DropParams& d) {
+  const uint64_t seed = d.rng[0], hi = d.rng[1] + d.site;
+  return DropKey{uint32_t(seed), uint32_t(seed >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+}
+
+__device__ __forceinline__ uint4 philox(const DropKey& k, uint64_t n) {
+  uint32_t c0 = uint32_t(n), c1 = uint32_t(n >> 32), c2 = k.c2, c3 = k.c3;
+  uint32_t k0 = k.k0, k1 = k.k1;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t p0 = uint64_t(c0) * 0xD2511F53u, p1 = uint64_t(c2) * 0xCD9E8D57u;
+    c0 = uint32_t(p1 >> 32) ^ c1 ^ k0;
+    c1 = uint32_t(p1);
+    c2 = uint32_t(p0 >> 32) ^ c3 ^ k1;
+    c3 = uint32_t(p0);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+// v[i] = kept ? v[i] * scale : 0 for the eight elements of group n.  A dropped
+// element is zero whatever it held (an infinity or a NaN included).
+__device__ __forceinline__ void drop8(const DropKey& k, uint64_t n, uint32_t thr, float scale,
+                                      float (&v)[8]) {
+  const uint4 u = philox(k, n);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t draw = (i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
+    v[i] = draw >= thr ? v[i] * scale : 0.0f;
+  }
+}
+
+}  // namespace stp

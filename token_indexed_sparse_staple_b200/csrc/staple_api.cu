@@ -708,4 +708,116 @@ staple_status staple_ffn_bwd(staple_context* ctx, staple_dtype dtype, int32_t T,
                           static_cast<float*>(dx), dw_gate, dw_up, dw_down, cs(stream));
 }
 
+// ------------------------------------------- around the layer: norm, dropout
+
+namespace {
+
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Required and optional tensors of the row operators: element-aligned.
+bool rows_ok(staple_dtype dt, std::initializer_list<const void*> need,
+             std::initializer_list<const void*> opt) {
+  for (const void* p : need)
+    if (!p || !aligned_to(p, esize(dt))) return false;
+  for (const void* p : opt)
+    if (!aligned_to(p, esize(dt))) return false;
+  return true;
+}
+
+staple_status check_rows(staple_dtype dt, int32_t T, int32_t D) {
+  if (dt != STAPLE_BF16 && dt != STAPLE_F32) return STAPLE_EINVAL;
+  return T < 0 || D <= 0 ? STAPLE_EINVAL : STAPLE_OK;
+}
+
+staple_status check_drop(const staple_drop* d) {
+  if (!d) return STAPLE_OK;
+  if (!(d->p >= 0.0 && d->p <= 1.0)) return STAPLE_EINVAL;   // refuses a NaN too
+  if (d->p > 0.0 && (!d->rng || !aligned_to(d->rng, 8))) return STAPLE_EINVAL;
+  return STAPLE_OK;
+}
+
+}  // namespace
+
+staple_status staple_norm_fwd(staple_context* ctx, staple_dtype dtype, staple_norm kind, int32_t T,
+                              int32_t D, const void* x, const void* residual,
+                              const staple_drop* drop, const void* weight, const void* bias,
+                              float eps, void* sum, void* y, float* mean, float* rstd,
+                              staple_stream stream) {
+  if (!ctx) return STAPLE_EINVAL;
+  STP_TRY(check_rows(dtype, T, D));
+  STP_TRY(check_drop(drop));
+  if (kind != STAPLE_NORM_LAYER && kind != STAPLE_NORM_RMS) return STAPLE_EINVAL;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return STAPLE_EINVAL;
+  if (D > stp::kNormMaxD) return STAPLE_EUNSUPPORTED;
+  if (T == 0) return STAPLE_OK;
+  if (!rows_ok(dtype, {x, y}, {residual, weight, bias, sum})) return STAPLE_EINVAL;
+  if (!aligned_to(mean, 4) || !aligned_to(rstd, 4)) return STAPLE_EINVAL;
+  if ((residual || (drop && drop->p > 0.0)) && !sum) return STAPLE_EINVAL;
+  if (sum == y) return STAPLE_EINVAL;
+  STP_TRY(set_device(ctx));
+  stp::TraceScope trace_scope(ctx->tracer);
+  return stp::launch_norm_fwd(dtype == STAPLE_BF16, kind == STAPLE_NORM_RMS, T, D, x, residual,
+                              drop, weight, bias, eps, sum, y, mean, rstd, cs(stream));
+}
+
+size_t staple_norm_workspace_bytes(int32_t T, int32_t D) {
+  if (T < 0 || D <= 0 || D > stp::kNormMaxD) return 0;
+  return (stp::norm_workspace_bytes(T, D) + 255) & ~size_t(255);
+}
+
+staple_status staple_norm_bwd(staple_context* ctx, staple_dtype dtype, staple_norm kind, int32_t T,
+                              int32_t D, const void* dy, const void* s, const void* weight,
+                              const float* mean, const float* rstd, const void* dsum_in,
+                              const staple_drop* drop, void* dsum, void* dx, float* dw, float* db,
+                              void* workspace, size_t workspace_bytes, staple_stream stream) {
+  if (!ctx) return STAPLE_EINVAL;
+  STP_TRY(check_rows(dtype, T, D));
+  STP_TRY(check_drop(drop));
+  if (kind != STAPLE_NORM_LAYER && kind != STAPLE_NORM_RMS) return STAPLE_EINVAL;
+  if (D > stp::kNormMaxD) return STAPLE_EUNSUPPORTED;
+  if (!aligned_to(dw, 4) || !aligned_to(db, 4)) return STAPLE_EINVAL;
+  if (T > 0) {
+    if (!rows_ok(dtype, {dy, s}, {weight, dsum_in, dsum, dx})) return STAPLE_EINVAL;
+    if (!rstd || !aligned_to(rstd, 4) || !aligned_to(mean, 4)) return STAPLE_EINVAL;
+    if (kind == STAPLE_NORM_LAYER && !mean) return STAPLE_EINVAL;
+    if (!dsum && !dx && !dw && !db) return STAPLE_EINVAL;
+    if (dsum && dsum == dx) return STAPLE_EINVAL;
+    if ((dw || db) && (!workspace || !aligned16(workspace) ||
+                       workspace_bytes < stp::norm_workspace_bytes(T, D)))
+      return STAPLE_EINVAL;
+  }
+  STP_TRY(set_device(ctx));
+  stp::TraceScope trace_scope(ctx->tracer);
+  return stp::launch_norm_bwd(ctx->di, dtype == STAPLE_BF16, kind == STAPLE_NORM_RMS, T, D, dy, s,
+                              weight, mean, rstd, dsum_in, drop, dsum, dx, dw, db,
+                              static_cast<float*>(workspace), cs(stream));
+}
+
+staple_status staple_dropout(staple_context* ctx, staple_dtype dtype, int32_t T, int32_t D,
+                             const void* x, const void* residual, const staple_drop* drop,
+                             void* out, staple_stream stream) {
+  if (!ctx || !drop) return STAPLE_EINVAL;
+  STP_TRY(check_rows(dtype, T, D));
+  STP_TRY(check_drop(drop));
+  if (T == 0) return STAPLE_OK;
+  if (!rows_ok(dtype, {x, out}, {residual})) return STAPLE_EINVAL;
+  STP_TRY(set_device(ctx));
+  stp::TraceScope trace_scope(ctx->tracer);
+  return stp::launch_dropout(dtype == STAPLE_BF16, T, D, x, residual, drop, out, cs(stream));
+}
+
+// --------------------------------------------------------- 8-bit products
+
+staple_status staple_quant_rows(staple_context* ctx, staple_dtype dtype, int32_t T, int32_t D,
+                                const void* x, int8_t* q, float* scale, staple_stream stream) {
+  if (!ctx) return STAPLE_EINVAL;
+  STP_TRY(check_rows(dtype, T, D));
+  if (D > stp::kQuantMaxD) return STAPLE_EUNSUPPORTED;
+  if (T == 0) return STAPLE_OK;
+  if (!rows_ok(dtype, {x}, {}) || !q || !scale || !aligned_to(scale, 4)) return STAPLE_EINVAL;
+  STP_TRY(set_device(ctx));
+  stp::TraceScope trace_scope(ctx->tracer);
+  return stp::launch_quant_rows(dtype == STAPLE_BF16, T, D, x, q, scale, cs(stream));
+}
+
 }  // extern "C"
