@@ -55,8 +55,10 @@ def _p(x) -> int | None:
 
 def _stream(s) -> int | None:
     if s is None:
+        # torch's current stream as a handle (torch.cuda.current_stream() builds
+        # a Stream object, 3 us a call)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream

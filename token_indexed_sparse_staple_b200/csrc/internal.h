@@ -118,20 +118,20 @@ staple_status tc_decode_fwd(const DeviceInfo& di, int T, int D, int F, const voi
 constexpr int kNormMaxD = 16384;
 constexpr int kNormMaxBlocks = 640;
 size_t norm_workspace_bytes(int T, int D);
-staple_status launch_norm_fwd(bool bf16, bool rms, int T, int D, const void* x, const void* res,
+staple_status launch_norm_fwd(const DeviceInfo& di, bool bf16, bool rms, int T, int D, const void* x, const void* res,
                               const staple_drop* drop, const void* w, const void* b, float eps,
                               void* sum, void* y, float* mean, float* rstd, cudaStream_t st);
 staple_status launch_norm_bwd(const DeviceInfo& di, bool bf16, bool rms, int T, int D,
                               const void* dy, const void* s, const void* w, const float* mean,
                               const float* rstd, const void* dsum_in, const staple_drop* drop,
                               void* dsum, void* dx, float* dw, float* db, float* part,
-                              cudaStream_t st);
+                              int32_t* err, cudaStream_t st);
 staple_status launch_dropout(bool bf16, int T, int D, const void* x, const void* res,
                              const staple_drop* drop, void* out, cudaStream_t st);
 
 // quant.cu: D is at most kQuantMaxD
 constexpr int kQuantMaxD = 32768;
-staple_status launch_quant_rows(bool bf16, int T, int D, const void* x, int8_t* q, float* scale,
+staple_status launch_quant_rows(const DeviceInfo& di, bool bf16, int T, int D, const void* x, int8_t* q, float* scale,
                                 cudaStream_t st);
 
 // simt_f32.cu (fp32 on CUDA cores)

@@ -17,6 +17,7 @@
 // in a second small kernel in block order, so the result does not depend on
 // timing.
 #include <algorithm>
+#include <atomic>
 
 #include "internal.h"
 #include "rows.cuh"
@@ -41,7 +42,8 @@ struct FwdParams {
 };
 
 template <bool BF16, int NV, bool VEC, bool DROP>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(const FwdParams p) {
+// (bf16: 64 registers, so that 32 warps share an SM)
+__global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdParams p) {
   __shared__ float red[2][32];
   const int rpb = blockDim.x / p.tpr;
   const int rg = threadIdx.x / p.tpr, t = threadIdx.x - rg * p.tpr;
@@ -60,69 +62,88 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const FwdParams p) {
       if (p.res) rr[i] = load_raw8<BF16, VEC>(p.res, base + e, n);
     }
   }
-  float v[NV][8];
-  float s1[1] = {0.0f};
+  F2 v[NV][4];
+  F2 s1 = f2(0.0f);
   DropKey key{};
   if (DROP) key = drop_key(p.drop);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int g = t + i * p.tpr;
+    float e[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = xr[i].get(j);
-    if (DROP) drop8(key, uint64_t(row) * uint64_t(G) + g, p.drop.thr, p.drop.scale, v[i]);
-    if (p.res)
+    for (int j = 0; j < 8; ++j) e[j] = xr[i].get(j);
+    if (DROP) drop8(key, uint64_t(row) * uint64_t(G) + g, p.drop.below, p.drop.scale, e);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] += rr[i].get(j);
+    for (int j = 0; j < 4; ++j) v[i][j] = f2(e[2 * j], e[2 * j + 1]);
     if (p.sum) {
       // the norm sees the sum as stored, which is what the backward pass reads
-      const Raw8<BF16> sr = pack_raw8<BF16>(v[i]);
+      // (a missing residual is zeros)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f2_get(v[i][j] + pair(rr[i], j), e[2 * j], e[2 * j + 1]);
+      const Raw8<BF16> sr = pack_raw8<BF16>(e);
       if (row_ok && g < G)
         store_raw8<BF16, VEC>(p.sum, base + g * kGroup, min(kGroup, p.D - g * kGroup), sr);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = sr.get(j);
+      for (int j = 0; j < 4; ++j) v[i][j] = pair(sr, j);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s1[0] += v[i][j];   // elements past D are zero
+    for (int j = 0; j < 4; ++j) s1 = s1 + v[i][j];   // elements past D are zero
   }
   const float inv_d = 1.0f / float(p.D);
   float mean = 0.0f;
   if (!p.rms) {
-    row_sum(s1, p.tpr, red[0]);
-    mean = s1[0] * inv_d;
+    float lo, hi;
+    f2_get(s1, lo, hi);
+    float a[1] = {lo + hi};
+    row_sum(a, p.tpr, red[0]);
+    mean = a[0] * inv_d;
   }
-  float s2[1] = {0.0f};
+  F2 s2 = f2(0.0f);
+  const F2 nmean = f2(-mean);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int left = p.D - (t + i * p.tpr) * kGroup;
+    if (VEC ? left > 0 : left >= kGroup) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < left) s2[0] = fmaf(v[i][j] - mean, v[i][j] - mean, s2[0]);
+      for (int j = 0; j < 4; ++j) {
+        v[i][j] = v[i][j] + nmean;
+        s2 = fma2(v[i][j], v[i][j], s2);
+      }
+    } else if (left > 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // the row's last, partial group: nothing past D counts
+        float lo, hi;
+        f2_get(v[i][j] + nmean, lo, hi);
+        v[i][j] = f2(2 * j < left ? lo : 0.0f, 2 * j + 1 < left ? hi : 0.0f);
+        s2 = fma2(v[i][j], v[i][j], s2);
+      }
+    }
   }
-  row_sum(s2, p.tpr, red[1]);
-  const float rstd = 1.0f / sqrtf(s2[0] * inv_d + p.eps);
+  float lo, hi;
+  f2_get(s2, lo, hi);
+  float a[1] = {lo + hi};
+  row_sum(a, p.tpr, red[1]);
+  const float rstd = 1.0f / sqrtf(a[0] * inv_d + p.eps);
   if (!row_ok) return;
   if (t == 0) {
     if (p.mean) p.mean[row] = mean;
     if (p.rstd) p.rstd[row] = rstd;
   }
+  const F2 rs = f2(rstd);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int g = t + i * p.tpr;
     if (g >= G) break;
     const int e = g * kGroup, n = min(kGroup, p.D - e);
+    // (a missing weight is ones, a missing bias is zeros)
+    Raw8<BF16> w = ones_raw8<BF16>(), b = zero_raw8<BF16>();
+    if (p.w) w = load_raw8<BF16, VEC>(p.w, e, n);
+    if (p.b) b = load_raw8<BF16, VEC>(p.b, e, n);
     float o[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = (v[i][j] - mean) * rstd;
-    if (p.w) {
-      const Raw8<BF16> w = load_raw8<BF16, VEC>(p.w, e, n);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] *= w.get(j);
-    }
-    if (p.b) {
-      const Raw8<BF16> b = load_raw8<BF16, VEC>(p.b, e, n);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] += b.get(j);
-    }
+    for (int j = 0; j < 4; ++j)
+      f2_get(fma2(v[i][j] * rs, pair(w, j), pair(b, j)), o[2 * j], o[2 * j + 1]);
     store_raw8<BF16, VEC>(p.y, base + e, n, pack_raw8<BF16>(o));
   }
 }
@@ -231,7 +252,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
         if (p.dsum) store_raw8<BF16, VEC>(p.dsum, row * p.D + e, n, pack_raw8<BF16>(d));
         if (p.dx) {
           // from the fp32 gradient, not from the rounded dsum
-          if (DROP) drop8(key, uint64_t(row) * uint64_t(G) + g, p.drop.thr, p.drop.scale, d);
+          if (DROP) drop8(key, uint64_t(row) * uint64_t(G) + g, p.drop.below, p.drop.scale, d);
           store_raw8<BF16, VEC>(p.dx, row * p.D + e, n, pack_raw8<BF16>(d));
         }
       }
@@ -272,6 +293,261 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
     }
 }
 
+// The same backward pass for rows of whole 16-byte words, with the rows
+// arriving by bulk asynchronous copies: tpr threads (whole warps) share a row
+// and walk the rows on their own, each group of threads with a ring of `stages`
+// rows per input tensor in shared memory, refilled by its first thread.  The
+// loads of the next rows are in flight while a row is summed and written, so
+// the memory stays busy through the two sums; groups meet only in their own
+// named barrier.
+//
+// The stage that a group refills after the barrier of row i is the one of row
+// i - 1: by then every thread of the group has left row i - 1 behind.
+//
+// NV groups of eight per thread and row, read from shared memory in both
+// passes.  Four of them make the two sums (10 shuffles and a barrier per row)
+// cheap against 32 elements and leave 128 registers enough for the 64 partial
+// sums of dw and db.
+struct RingParams {
+  BwdParams b;
+  int32_t stages, tensors;   // tensors: 2, or 3 with dsum_in
+  int32_t row_bytes;
+  int32_t* err;
+  uint64_t wait_ns;
+};
+
+constexpr int kRingMaxGroups = 8;    // row groups per block
+constexpr int kRingMaxStages = 4;
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void group_sync(int rg, int tpr) {
+  if (tpr == 32) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(rg + 1), "r"(tpr) : "memory");
+}
+
+template <bool BF16, int NV, bool DROP>
+__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp) {
+  // what both passes use stays in registers where the partial sums leave room
+  constexpr bool KEEP = NV <= 2;
+  const BwdParams& p = rp.b;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[kRingMaxGroups][kRingMaxStages];
+  __shared__ float2 red[2][16];       // [parity][warp]
+  __shared__ int abort_flag;
+  const int rpb = blockDim.x / p.tpr;
+  const int rg = threadIdx.x / p.tpr, t = threadIdx.x - rg * p.tpr;
+  const int G = p.D / kGroup;
+  const int S = rp.stages, nt = rp.tensors;
+  const int64_t stage_bytes = int64_t(rp.row_bytes) * nt;
+  uint8_t* ring = smem + rg * S * stage_bytes;
+  uint64_t* full = bars[rg];
+  volatile int* abort = &abort_flag;
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < rpb; ++g)
+      for (int s = 0; s < S; ++s) mbar_init(&bars[g][s], 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int64_t row0 = int64_t(blockIdx.x) * rpb + rg, step = int64_t(gridDim.x) * rpb;
+  auto fill = [&](int64_t row, int s) {
+    uint8_t* dst = ring + s * stage_bytes;
+    const int64_t off = row * rp.row_bytes;
+    mbar_arrive_expect_tx(&full[s], uint32_t(stage_bytes));
+    bulk_load(dst, static_cast<const uint8_t*>(p.dy) + off, rp.row_bytes, &full[s]);
+    bulk_load(dst + rp.row_bytes, static_cast<const uint8_t*>(p.s) + off, rp.row_bytes, &full[s]);
+    if (nt > 2)
+      bulk_load(dst + 2 * int64_t(rp.row_bytes), static_cast<const uint8_t*>(p.dsum_in) + off,
+                rp.row_bytes, &full[s]);
+  };
+  if (t == 0)
+    for (int s = 0; s < S; ++s)
+      if (row0 + s * step < p.T) fill(row0 + s * step, s);
+  const float inv_d = 1.0f / float(p.D);
+  F2 aw[NV][4], ab[NV][4];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) aw[i][j] = ab[i][j] = f2(0.0f);
+  // (a missing weight is multiplied as ones, a missing gradient added as
+  // zeros below: a test per pair would put a branch around each)
+  F2 ws[KEEP ? NV : 1][4];
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Raw8<BF16> w = ones_raw8<BF16>();
+      if (p.w && t + i * p.tpr < G)
+        w = load_raw8<BF16, true>(p.w, (t + i * p.tpr) * kGroup, kGroup);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ws[i][j] = pair(w, j);
+    }
+  }
+  DropKey key{};
+  if (DROP) key = drop_key(p.drop);
+  int st = 0, par = 0;
+  uint32_t ph = 0;
+  // a row's mean and rstd are loaded a row ahead, out of the way of its sums
+  float mu_next = 0.0f, rs_next = 0.0f;
+  auto fetch = [&](int64_t row) {
+    if (row >= p.T) return;
+    if (!p.rms) mu_next = p.mean[row];
+    rs_next = p.rstd[row];
+  };
+  fetch(row0);
+  for (int64_t row = row0; row < p.T; row += step, par ^= 1) {
+    const float mu = mu_next, rs = rs_next;
+    fetch(row + step);
+    // After a wait that ran out the group goes on with what the stage holds
+    // (its outputs are then undefined); the flag ends every later wait.
+    mbar_wait(&full[st], ph, abort, rp.err, rp.wait_ns);
+    const uint8_t* src = ring + st * stage_bytes;
+    F2 c1 = f2(0.0f), c2 = f2(0.0f);
+    const F2 nmu = f2(-mu), rs2 = f2(rs);
+    F2 gws[KEEP ? NV : 1][4], xhs[KEEP ? NV : 1][4];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int g = t + i * p.tpr;
+      if (g < G) {
+        const Raw8<BF16> dyr = load_raw8<BF16, true>(src, g * kGroup, kGroup);
+        const Raw8<BF16> sr = load_raw8<BF16, true>(src + rp.row_bytes, g * kGroup, kGroup);
+        Raw8<BF16> w = ones_raw8<BF16>();
+        if (!KEEP && p.w) w = load_raw8<BF16, true>(p.w, g * kGroup, kGroup);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const F2 dy = pair(dyr, j), xh = (pair(sr, j) + nmu) * rs2;
+          const F2 gw = dy * (KEEP ? ws[KEEP ? i : 0][j] : pair(w, j));
+          aw[i][j] = fma2(dy, xh, aw[i][j]);
+          ab[i][j] = ab[i][j] + dy;
+          c1 = c1 + gw;
+          c2 = fma2(gw, xh, c2);
+          if (KEEP) {
+            gws[KEEP ? i : 0][j] = gw;
+            xhs[KEEP ? i : 0][j] = xh;
+          }
+        }
+      }
+    }
+    float a0, a1, b0, b1;
+    f2_get(c1, a0, a1);
+    f2_get(c2, b0, b1);
+    a0 += a1;
+    b0 += b1;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+      a0 += __shfl_xor_sync(0xffffffffu, a0, m);
+      b0 += __shfl_xor_sync(0xffffffffu, b0, m);
+    }
+    if (p.tpr > 32) {
+      const int warp = threadIdx.x >> 5, wpr = p.tpr >> 5, w0 = warp / wpr * wpr;
+      if ((threadIdx.x & 31) == 0) red[par][warp] = make_float2(a0, b0);
+      group_sync(rg, p.tpr);
+      a0 = b0 = 0.0f;
+      for (int k = 0; k < wpr; ++k) {
+        const float2 v = red[par][w0 + k];
+        a0 += v.x;
+        b0 += v.y;
+      }
+    } else {
+      __syncwarp();
+    }
+    // row - step is behind every thread of the group: its stage takes the
+    // row S - 1 steps ahead of this one
+    if (t == 0 && row != row0 && row + (S - 1) * step < p.T)
+      fill(row + (S - 1) * step, st == 0 ? S - 1 : st - 1);
+    const F2 nc1 = f2(p.rms ? 0.0f : -a0 * inv_d), nc2 = f2(-b0 * inv_d);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int g = t + i * p.tpr;
+      if (g >= G) break;
+      Raw8<BF16> dyr, sr, w = ones_raw8<BF16>(), add = zero_raw8<BF16>();
+      if (!KEEP) {
+        dyr = load_raw8<BF16, true>(src, g * kGroup, kGroup);
+        sr = load_raw8<BF16, true>(src + rp.row_bytes, g * kGroup, kGroup);
+        if (p.w) w = load_raw8<BF16, true>(p.w, g * kGroup, kGroup);
+      }
+      if (nt > 2) add = load_raw8<BF16, true>(src + 2 * int64_t(rp.row_bytes), g * kGroup, kGroup);
+      float d[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        F2 gw, xh;
+        if constexpr (KEEP) {
+          gw = gws[i][j];
+          xh = xhs[i][j];
+        } else {
+          xh = (pair(sr, j) + nmu) * rs2;
+          gw = pair(dyr, j) * pair(w, j);
+        }
+        const F2 ds = fma2(fma2(xh, nc2, gw + nc1), rs2, pair(add, j));
+        f2_get(ds, d[2 * j], d[2 * j + 1]);
+      }
+      const int64_t off = row * p.D + g * kGroup;
+      if (p.dsum) store_raw8<BF16, true>(p.dsum, off, kGroup, pack_raw8<BF16>(d));
+      if (p.dx) {
+        // from the fp32 gradient, not from the rounded dsum
+        if (DROP) drop8(key, uint64_t(row) * uint64_t(G) + g, p.drop.below, p.drop.scale, d);
+        store_raw8<BF16, true>(p.dx, off, kGroup, pack_raw8<BF16>(d));
+      }
+    }
+    if (++st == S) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+  // every fill was waited for above, unless a wait ran out: then let the
+  // copies in flight land before the shared memory goes away
+  if (*abort && t == 0)
+    for (int s = 0; s < S; ++s) mbar_drain(&full[s], s < st ? ph : ph ^ 1);
+  if (!p.part) return;
+  float* out = p.part + int64_t(blockIdx.x) * 2 * p.D;
+  if (rpb == 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int g = t + i * p.tpr;
+      if (g >= G) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float lo, hi;
+        f2_get(aw[i][j], lo, hi);
+        *reinterpret_cast<float2*>(out + g * kGroup + 2 * j) = make_float2(lo, hi);
+        f2_get(ab[i][j], lo, hi);
+        *reinterpret_cast<float2*>(out + p.D + g * kGroup + 2 * j) = make_float2(lo, hi);
+      }
+    }
+    return;
+  }
+  // the block's row groups add up in group order, [row group][2][D] floats
+  // over the rings, which no copy writes any more
+  __syncthreads();
+  float* acc = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int g = t + i * p.tpr;
+    if (g >= G) break;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      f2_get(aw[i][j], lo, hi);
+      *reinterpret_cast<float2*>(acc + (rg * 2 + 0) * p.D + g * kGroup + 2 * j) = make_float2(lo, hi);
+      f2_get(ab[i][j], lo, hi);
+      *reinterpret_cast<float2*>(acc + (rg * 2 + 1) * p.D + g * kGroup + 2 * j) = make_float2(lo, hi);
+    }
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < 2 * p.D; k += blockDim.x) {
+    float s = 0.0f;
+    for (int q = 0; q < rpb; ++q) s += acc[q * 2 * p.D + k];
+    out[k] = s;
+  }
+}
+
 // dw[d], db[d] = sums over the blocks of the backward kernel, in block order
 // within each of 8 slices, then over the slices in order.  Block: 32 columns
 // x 8 slices.
@@ -300,6 +576,16 @@ __global__ void __launch_bounds__(kWgCols* kWgSlices)
 }
 
 inline int cdiv(int64_t a, int64_t b) { return int((a + b - 1) / b); }
+
+// Groups per thread of the forward kernel: with few rows one, so that a row is
+// as many threads wide as it can be and its chain of loads and sums as short;
+// with many four, so that the two sums across threads cost little per element
+// and each thread has four loads per tensor in flight.
+int row_groups_per_thread(int G, int T, int num_sms) {
+  if (G > 1024) return 4;
+  if (T <= 2 * num_sms) return G > 512 ? 2 : 1;
+  return G > 64 ? 4 : (G > 32 ? 2 : 1);
+}
 
 bool vec_ok(int D, std::initializer_list<const void*> ps) {
   if (D % kGroup) return false;
@@ -346,14 +632,71 @@ staple_status bwd_nv(const BwdParams& p, int nv, int grid, int block, size_t sme
   }
 }
 
+// The ring kernel's launch: block, stages, blocks per SM and shared memory;
+// false where the rows do not suit it (then the plain kernel runs).
+struct RingPlan {
+  int nv, tpr, rpb, stages, per_sm;
+  size_t smem;
+};
+bool plan_ring(int D, int es, int tensors, RingPlan* out) {
+  const int G = D / kGroup;
+  RingPlan r{};
+  // fp32 groups are twice as wide: four per thread would not leave the
+  // partial sums their registers (only rows beyond 8192 need them)
+  r.nv = G > 1024 ? 4 : (G > 32 ? 2 : 1);
+  r.tpr = std::max(32, threads_per_row(G, r.nv));
+  r.rpb = std::max(1, 256 / r.tpr);
+  const size_t row_stage = size_t(D) * es * tensors * r.rpb;
+  for (r.per_sm = std::max(1, 512 / (r.rpb * r.tpr)); r.per_sm >= 1; --r.per_sm) {
+    // 228 KB per SM, of which each block's share loses 1 KB to the system and
+    // under 1 KB to static arrays; 227 KB at most per block
+    const size_t avail = std::min<size_t>(size_t(228) * 1024 / r.per_sm - 2048, 226 * 1024);
+    r.stages = int(std::min<size_t>(kRingMaxStages, avail / row_stage));
+    if (r.stages >= 2) {
+      r.smem = row_stage * r.stages;
+      *out = r;
+      return true;
+    }
+  }
+  return false;
+}
+
+template <bool BF16, int NV, bool DROP>
+staple_status ring_go(const DeviceInfo& di, const RingParams& p, int grid, int block, size_t smem,
+                      cudaStream_t st) {
+  auto kern = norm_bwd_ring_kernel<BF16, NV, DROP>;
+  // set once per device, so that no attribute call happens during a capture
+  static std::atomic<uint64_t> attr_done{0};
+  const uint64_t bit = uint64_t(1) << (di.device & 63);
+  if (!(attr_done.load() & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) !=
+        cudaSuccess)
+      return STAPLE_ECUDA;
+    attr_done.fetch_or(bit);
+  }
+  STP_LAUNCH("norm_bwd", st, kern<<<grid, block, smem, st>>>(p));
+  return cudaGetLastError() == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+}
+
+template <bool BF16, bool DROP>
+staple_status ring_nv(const DeviceInfo& di, const RingParams& p, int nv, int grid, int block,
+                      size_t smem, cudaStream_t st) {
+  switch (nv) {
+    case 1: return ring_go<BF16, 1, DROP>(di, p, grid, block, smem, st);
+    case 2: return ring_go<BF16, 2, DROP>(di, p, grid, block, smem, st);
+    default: return ring_go<BF16, 4, DROP>(di, p, grid, block, smem, st);
+  }
+}
+
 DropParams drop_params(const staple_drop* d) {
   DropParams r{};
   if (!d) return r;
-  r.thr = uint32_t(d->p * 65536.0 + 0.5);
-  if (r.thr == 0) return r;
+  const uint32_t thr = uint32_t(d->p * 65536.0 + 0.5);
+  if (thr == 0) return r;
+  r.below = uint32_t((uint64_t(thr) << 16) - 1);
   r.rng = static_cast<const uint64_t*>(d->rng);
   r.site = d->site;
-  r.scale = r.thr < 65536 ? float(65536.0 / double(65536 - r.thr)) : 0.0f;
+  r.scale = thr < 65536 ? float(65536.0 / double(65536 - thr)) : 0.0f;
   return r;
 }
 
@@ -386,7 +729,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams p) {
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = xr.get(j);
-  if (DROP) drop8(drop_key(p.drop), uint64_t(u), p.drop.thr, p.drop.scale, v);
+  if (DROP) drop8(drop_key(p.drop), uint64_t(u), p.drop.below, p.drop.scale, v);
   if (p.res)
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += rr.get(j);
@@ -409,15 +752,15 @@ size_t norm_workspace_bytes(int T, int D) {
   return size_t(std::min(T, kNormMaxBlocks)) * 2 * size_t(D) * sizeof(float);
 }
 
-staple_status launch_norm_fwd(bool bf16, bool rms, int T, int D, const void* x, const void* res,
+staple_status launch_norm_fwd(const DeviceInfo& di, bool bf16, bool rms, int T, int D, const void* x, const void* res,
                               const staple_drop* drop, const void* w, const void* b, float eps,
                               void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
   if (T == 0) return STAPLE_OK;
   FwdParams p{x, res, w, b, sum, y, mean, rstd, drop_params(drop), T, D, 0, eps, rms};
   const int G = groups_of(D);
-  const int nv = G <= 512 ? 1 : (G <= 1024 ? 2 : 4);
+  const int nv = row_groups_per_thread(G, T, di.num_sms);
   p.tpr = threads_per_row(G, nv);
-  const int rpb = std::max(1, 256 / p.tpr);
+  const int rpb = std::max(1, 128 / p.tpr);
   const int grid = cdiv(T, rpb), block = rpb * p.tpr;
   const bool vec = vec_ok(D, {x, res, w, b, sum, y});
   if (bf16) return vec ? fwd_nv<true, true>(p, nv, grid, block, st)
@@ -430,7 +773,7 @@ staple_status launch_norm_bwd(const DeviceInfo& di, bool bf16, bool rms, int T, 
                               const void* dy, const void* s, const void* w, const float* mean,
                               const float* rstd, const void* dsum_in, const staple_drop* drop,
                               void* dsum, void* dx, float* dw, float* db, float* part,
-                              cudaStream_t st) {
+                              int32_t* err, cudaStream_t st) {
   if (T == 0) {
     if (dw && cudaMemsetAsync(dw, 0, size_t(D) * 4, st) != cudaSuccess) return STAPLE_ECUDA;
     if (db && cudaMemsetAsync(db, 0, size_t(D) * 4, st) != cudaSuccess) return STAPLE_ECUDA;
@@ -439,26 +782,41 @@ staple_status launch_norm_bwd(const DeviceInfo& di, bool bf16, bool rms, int T, 
   BwdParams p{dy, s, w, mean, rstd, dsum_in, dsum, dx, (dw || db) ? part : nullptr,
               drop_params(drop), T, D, 0, rms};
   const int G = groups_of(D);
-  const int nv = G <= 512 ? 1 : (G <= 1024 ? 2 : 4);
-  p.tpr = threads_per_row(G, nv);
-  const int rpb = std::max(1, 256 / p.tpr);
-  const int block = rpb * p.tpr;
-  const int R = rows_in_flight(bf16, nv);
-  const int grid = std::min(std::min(cdiv(T, int64_t(rpb) * R), kNormMaxBlocks),
-                            di.num_sms * std::max(1, 512 / block));
-  const size_t smem = rpb > 1 ? size_t(rpb) * 2 * p.tpr * nv * kGroup * sizeof(float) : 0;
   const bool vec = vec_ok(D, {dy, s, w, dsum_in, dsum, dx});
   staple_status r;
-  if (bf16)
-    r = vec ? (p.drop.rng ? bwd_nv<true, true, true>(p, nv, grid, block, smem, st)
-                          : bwd_nv<true, true, false>(p, nv, grid, block, smem, st))
-            : (p.drop.rng ? bwd_nv<true, false, true>(p, nv, grid, block, smem, st)
-                          : bwd_nv<true, false, false>(p, nv, grid, block, smem, st));
-  else
-    r = vec ? (p.drop.rng ? bwd_nv<false, true, true>(p, nv, grid, block, smem, st)
-                          : bwd_nv<false, true, false>(p, nv, grid, block, smem, st))
-            : (p.drop.rng ? bwd_nv<false, false, true>(p, nv, grid, block, smem, st)
-                          : bwd_nv<false, false, false>(p, nv, grid, block, smem, st));
+  int grid;
+  RingPlan rp;
+  if (vec && G >= 32 && plan_ring(D, bf16 ? 2 : 4, dsum_in ? 3 : 2, &rp)) {
+    p.tpr = rp.tpr;
+    grid = std::min(std::min(cdiv(T, rp.rpb), kNormMaxBlocks), di.num_sms * rp.per_sm);
+    const RingParams q{p, rp.stages, dsum_in ? 3 : 2, D * (bf16 ? 2 : 4), err, di.wait_ns};
+    const int block = rp.rpb * rp.tpr;
+    if (bf16)
+      r = p.drop.rng ? ring_nv<true, true>(di, q, rp.nv, grid, block, rp.smem, st)
+                     : ring_nv<true, false>(di, q, rp.nv, grid, block, rp.smem, st);
+    else
+      r = p.drop.rng ? ring_nv<false, true>(di, q, rp.nv, grid, block, rp.smem, st)
+                     : ring_nv<false, false>(di, q, rp.nv, grid, block, rp.smem, st);
+  } else {
+    const int nv = G <= 512 ? 1 : (G <= 1024 ? 2 : 4);
+    p.tpr = threads_per_row(G, nv);
+    const int rpb = std::max(1, 256 / p.tpr);
+    const int block = rpb * p.tpr;
+    const int R = rows_in_flight(bf16, nv);
+    grid = std::min(std::min(cdiv(T, int64_t(rpb) * R), kNormMaxBlocks),
+                    di.num_sms * std::max(1, 512 / block));
+    const size_t smem = rpb > 1 ? size_t(rpb) * 2 * p.tpr * nv * kGroup * sizeof(float) : 0;
+    if (bf16)
+      r = vec ? (p.drop.rng ? bwd_nv<true, true, true>(p, nv, grid, block, smem, st)
+                            : bwd_nv<true, true, false>(p, nv, grid, block, smem, st))
+              : (p.drop.rng ? bwd_nv<true, false, true>(p, nv, grid, block, smem, st)
+                            : bwd_nv<true, false, false>(p, nv, grid, block, smem, st));
+    else
+      r = vec ? (p.drop.rng ? bwd_nv<false, true, true>(p, nv, grid, block, smem, st)
+                            : bwd_nv<false, true, false>(p, nv, grid, block, smem, st))
+              : (p.drop.rng ? bwd_nv<false, false, true>(p, nv, grid, block, smem, st)
+                            : bwd_nv<false, false, false>(p, nv, grid, block, smem, st));
+  }
   if (r != STAPLE_OK || !p.part) return r;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cdiv(D, kWgCols), 2);

@@ -43,7 +43,8 @@ __device__ __forceinline__ uint32_t q_exact(float x, double scale) {
 }
 
 template <bool BF16, int NV, bool VEC>
-__global__ void __launch_bounds__(1024) quant_rows_kernel(const QuantParams p) {
+// (bf16: 64 registers, so that 32 warps share an SM)
+__global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const QuantParams p) {
   __shared__ uint32_t red[32];
   const int rpb = blockDim.x / p.tpr;
   const int rg = threadIdx.x / p.tpr, t = threadIdx.x - rg * p.tpr;
@@ -62,10 +63,19 @@ __global__ void __launch_bounds__(1024) quant_rows_kernel(const QuantParams p) {
   // the largest |x| as bits: a NaN is above the infinity, which is above
   // every finite number
   uint32_t m = 0;
+  if constexpr (BF16) {
+    // two bf16 magnitudes at a time as 16-bit integers
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(xr[i].get(j)) & 0x7fffffffu);
+      for (int j = 0; j < 4; ++j) m = __vmaxu2(m, xr[i].w[j] & 0x7fff7fffu);
+    m = max(m << 16, m & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, xr[i].w[j] & 0x7fffffffu);
+  }
   if (p.tpr >= 32) {
     m = __reduce_max_sync(0xffffffffu, m);
     if (p.tpr > 32) {
@@ -83,25 +93,33 @@ __global__ void __launch_bounds__(1024) quant_rows_kernel(const QuantParams p) {
   const float scale = amax / 127.0f;
   const bool finite = m < 0x7f800000u;
   if (t == 0) p.scale[row] = scale;
-  const float inv = 1.0f / scale, half = 0.5f * scale;
+  // (an approximate reciprocal will do: the remainder decides)
+  const F2 inv = f2(__fdividef(1.0f, scale)), nscale = f2(-scale);
+  const F2 magic = f2(kRintMagic), nmagic = f2(-kRintMagic);
+  const bool fast = finite && amax >= kTiny;
+  const float half = fast ? 0.5f * scale : 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int g = t + i * p.tpr;
     if (g >= G) break;
+    float worst = 0.0f;
     uint32_t b[8];
-    bool exact = false;
-    if (finite && amax >= kTiny) {
-      float worst = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = xr[i].get(j);
-        const float s = fmaf(x, inv, kRintMagic);
-        worst = fmaxf(worst, fabsf(fmaf(-(s - kRintMagic), scale, x)));
-        b[j] = __float_as_uint(s) & 0xffu;
-      }
-      exact = worst < half;
+    for (int j = 0; j < 4; ++j) {
+      const F2 x = pair(xr[i], j);
+      const F2 s = fma2(x, inv, magic);
+      float r0, r1, s0, s1;
+      f2_get(fma2(s + nmagic, nscale, x), r0, r1);
+      f2_get(s, s0, s1);
+      worst = fmaxf(worst, fmaxf(fabsf(r0), fabsf(r1)));
+      b[2 * j] = __float_as_uint(s0);
+      b[2 * j + 1] = __float_as_uint(s1);
     }
-    if (!exact) {
+    // the low bytes of four words
+    uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    if (!(worst < half)) {
+      lo = hi = 0;
 #pragma unroll 1
       for (int j = 0; j < 8; ++j) {
         float x = 0.0f;
@@ -109,21 +127,18 @@ __global__ void __launch_bounds__(1024) quant_rows_kernel(const QuantParams p) {
         for (int k = 0; k < 8; ++k)
           if (k == j) x = xr[i].get(k);
         const uint32_t v = finite && scale > 0.0f ? q_exact(x, double(scale)) : 0u;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k == j) b[k] = v;
+        if (j < 4) lo |= v << (8 * j);
+        else hi |= v << (8 * j - 32);
       }
     }
     int8_t* dst = p.q + base + g * kGroup;
-    const uint32_t lo = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
-    const uint32_t hi = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
     if constexpr (VEC) {
       *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
     } else {
       const int n = min(kGroup, p.D - g * kGroup);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < n) dst[j] = int8_t(b[j]);
+        if (j < n) dst[j] = int8_t((j < 4 ? lo >> (8 * j) : hi >> (8 * j - 32)) & 0xffu);
     }
   }
 }
@@ -133,20 +148,26 @@ void go(const QuantParams& p, int nv, unsigned grid, int block, cudaStream_t st)
   switch (nv) {
     case 1: quant_rows_kernel<BF16, 1, VEC><<<grid, block, 0, st>>>(p); break;
     case 2: quant_rows_kernel<BF16, 2, VEC><<<grid, block, 0, st>>>(p); break;
-    default: quant_rows_kernel<BF16, 4, VEC><<<grid, block, 0, st>>>(p); break;
+    case 4: quant_rows_kernel<BF16, 4, VEC><<<grid, block, 0, st>>>(p); break;
+    default: quant_rows_kernel<BF16, 8, VEC><<<grid, block, 0, st>>>(p); break;
   }
 }
 
 }  // namespace
 
-staple_status launch_quant_rows(bool bf16, int T, int D, const void* x, int8_t* q, float* scale,
+staple_status launch_quant_rows(const DeviceInfo& di, bool bf16, int T, int D, const void* x, int8_t* q, float* scale,
                                 cudaStream_t st) {
   if (T == 0) return STAPLE_OK;
   QuantParams p{x, q, scale, T, D, 0};
   const int G = groups_of(D);
-  const int nv = G <= 1024 ? 1 : (G <= 2048 ? 2 : 4);
+  // few rows: as many threads per row as there are groups; many: up to eight
+  // groups per thread, whose loads are in flight together and whose maximum
+  // is found with few instructions per element
+  const int few = G > 2048 ? 8 : (G > 1024 ? 4 : (G > 512 ? 2 : 1));
+  const int many = G > 128 ? 8 : (G > 64 ? 4 : (G > 32 ? 2 : 1));
+  const int nv = T <= 2 * di.num_sms ? few : many;
   p.tpr = threads_per_row(G, nv);
-  const int rpb = std::max(1, 256 / p.tpr);
+  const int rpb = std::max(1, 128 / p.tpr);
   const unsigned grid = unsigned((int64_t(T) + rpb - 1) / rpb);
   const int block = rpb * p.tpr;
   const bool vec = D % kGroup == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 &&

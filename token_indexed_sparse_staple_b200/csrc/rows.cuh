@@ -60,6 +60,14 @@ __device__ __forceinline__ Raw8<BF16> zero_raw8() {
   return r;
 }
 
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> ones_raw8() {
+  Raw8<BF16> r;
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 4 : 8); ++i) r.w[i] = BF16 ? 0x3f803f80u : 0x3f800000u;
+  return r;
+}
+
 // Eight floats rounded to the element type (bf16: to nearest even, the
 // storage rounding of every bf16 tensor of the library).
 template <bool BF16>
@@ -152,7 +160,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float* red) {
 struct DropParams {
   const uint64_t* rng;   // device {seed, offset}; NULL: no dropout
   uint64_t site;
-  uint32_t thr;          // keep if draw >= thr (65536: keep nothing)
+  uint32_t below;        // thr * 2^16 - 1: a draw in a word's high half is kept if word > below
   float scale;           // 65536 / (65536 - thr)
 };
 
@@ -161,7 +169,10 @@ struct DropKey {
 };
 
 __device__ __forceinline__ DropKey drop_key(const DropParams& d) {
-  const uint64_t seed = d.rng[0], hi = d.rng[1] + d.site;
+  // (read-only loads: with them the compiler knows the key to be the same in
+  // every thread and keeps its schedule out of the vector registers)
+  const unsigned long long* r = reinterpret_cast<const unsigned long long*>(d.rng);
+  const uint64_t seed = __ldg(r), hi = __ldg(r + 1) + d.site;
   return DropKey{uint32_t(seed), uint32_t(seed >> 32), uint32_t(hi), uint32_t(hi >> 32)};
 }
 
@@ -182,16 +193,56 @@ __device__ __forceinline__ uint4 philox(const DropKey& k, uint64_t n) {
 }
 
 // v[i] = kept ? v[i] * scale : 0 for the eight elements of group n.  A dropped
-// element is zero whatever it held (an infinity or a NaN included).
-__device__ __forceinline__ void drop8(const DropKey& k, uint64_t n, uint32_t thr, float scale,
+// element is zero whatever it held (an infinity or a NaN included).  A draw in
+// the high half is compared without taking it out of its word; thr = 2^16
+// makes `below` the largest word, which no word exceeds.
+__device__ __forceinline__ void drop8(const DropKey& k, uint64_t n, uint32_t below, float scale,
                                       float (&v)[8]) {
   const uint4 u = philox(k, n);
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t draw = (i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
-    v[i] = draw >= thr ? v[i] * scale : 0.0f;
+    const uint32_t draw = (i & 1) ? w[i >> 1] : w[i >> 1] << 16;
+    v[i] = draw > below ? v[i] * scale : 0.0f;
   }
+}
+
+// ---------------------------------------------------------------------------
+// Pairs of floats (fma.rn.f32x2 and friends): two IEEE operations in one
+// instruction, which the row kernels need because they are close to bound by
+// instruction issue.
+// ---------------------------------------------------------------------------
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void f2_get(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// Elements 2j and 2j + 1 of a group.
+template <bool BF16>
+__device__ __forceinline__ F2 pair(const Raw8<BF16>& r, int j) {
+  return f2(r.get(2 * j), r.get(2 * j + 1));
 }
 
 }  // namespace stp

@@ -756,7 +756,7 @@ staple_status staple_norm_fwd(staple_context* ctx, staple_dtype dtype, staple_no
   if (sum == y) return STAPLE_EINVAL;
   STP_TRY(set_device(ctx));
   stp::TraceScope trace_scope(ctx->tracer);
-  return stp::launch_norm_fwd(dtype == STAPLE_BF16, kind == STAPLE_NORM_RMS, T, D, x, residual,
+  return stp::launch_norm_fwd(ctx->di, dtype == STAPLE_BF16, kind == STAPLE_NORM_RMS, T, D, x, residual,
                               drop, weight, bias, eps, sum, y, mean, rstd, cs(stream));
 }
 
@@ -790,7 +790,7 @@ staple_status staple_norm_bwd(staple_context* ctx, staple_dtype dtype, staple_no
   stp::TraceScope trace_scope(ctx->tracer);
   return stp::launch_norm_bwd(ctx->di, dtype == STAPLE_BF16, kind == STAPLE_NORM_RMS, T, D, dy, s,
                               weight, mean, rstd, dsum_in, drop, dsum, dx, dw, db,
-                              static_cast<float*>(workspace), cs(stream));
+                              static_cast<float*>(workspace), ctx->d_err, cs(stream));
 }
 
 staple_status staple_dropout(staple_context* ctx, staple_dtype dtype, int32_t T, int32_t D,
@@ -817,7 +817,7 @@ staple_status staple_quant_rows(staple_context* ctx, staple_dtype dtype, int32_t
   if (!rows_ok(dtype, {x}, {}) || !q || !scale || !aligned_to(scale, 4)) return STAPLE_EINVAL;
   STP_TRY(set_device(ctx));
   stp::TraceScope trace_scope(ctx->tracer);
-  return stp::launch_quant_rows(dtype == STAPLE_BF16, T, D, x, q, scale, cs(stream));
+  return stp::launch_quant_rows(ctx->di, dtype == STAPLE_BF16, T, D, x, q, scale, cs(stream));
 }
 
 }  // extern "C"
