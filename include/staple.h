@@ -510,6 +510,19 @@ staple_status staple_dropout(staple_context* ctx, staple_dtype dtype, int32_t T,
 staple_status staple_quant_rows(staple_context* ctx, staple_dtype dtype, int32_t T, int32_t D,
                                 const void* x, int8_t* q, float* scale, staple_stream stream);
 
+/* y[t][n] = (sum_k a[t][k] b[n][k]) a_scale[t] b_scale[n], on the tensor cores:
+ * the sum is exact (32-bit integers), then rounded to fp32, multiplied by the
+ * two scales in fp32 and rounded to dtype.
+ *   a        int8 [T][K], b  int8 [N][K]; every value of 8 bits is allowed;
+ *            16-byte aligned
+ *   a_scale  fp32 [T], b_scale  fp32 [N]
+ *   y        out [T][N] (dtype); must not overlap the inputs
+ * K is a multiple of 16 (EINVAL) and at most 131056 (EUNSUPPORTED); T >= 0 and
+ * N >= 1 are any.  No workspace; one launch. */
+staple_status staple_matmul_i8(staple_context* ctx, staple_dtype dtype, int32_t T, int32_t N,
+                               int32_t K, const int8_t* a, const float* a_scale, const int8_t* b,
+                               const float* b_scale, void* y, staple_stream stream);
+
 /* ------------------------------------------------ host optimizer (AdamW) */
 
 typedef struct staple_adamw {

@@ -110,3 +110,15 @@ def test_quant_rows(lib, ctx):
         (dict(D=32769), U), (dict(x=None), E), (dict(q=None), E), (dict(scale=None), E),
         (dict(x=ODD), E), (dict(scale=OK_PTR + 2), E), (dict(T=0), stp.STAPLE_OK),
     ])
+
+
+def test_matmul_i8(lib, ctx):
+    good = dict(ctx=ctx, dtype=F32, T=3, N=5, K=32, a=OK_PTR, a_scale=OK_PTR, b=OK_PTR,
+                b_scale=OK_PTR + 4, y=OK_PTR + 4, stream=None)
+    check(lib.staple_matmul_i8, good, [
+        (dict(ctx=None), E), (dict(dtype=2), E), (dict(T=-1), E), (dict(N=0), E), (dict(N=-1), E),
+        (dict(K=0), E), (dict(K=8), E), (dict(K=-16), E), (dict(K=33), E), (dict(K=131072), U),
+        (dict(a=None), E), (dict(b=None), E), (dict(a_scale=None), E), (dict(b_scale=None), E),
+        (dict(y=None), E), (dict(a=OK_PTR + 8), E), (dict(b=ODD), E), (dict(a_scale=OK_PTR + 2), E),
+        (dict(b_scale=ODD), E), (dict(y=OK_PTR + 2), E), (dict(T=0), stp.STAPLE_OK),
+    ])

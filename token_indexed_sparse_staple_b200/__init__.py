@@ -325,3 +325,9 @@ def staple_quant_rows(ctx, dtype, T, D, x, q, scale, stream=None):
     """Rows to 8-bit integers with one scale each (see include/staple.h)."""
     _ok(lib().staple_quant_rows(ctx, dtype, T, D, _p(x), _p(q), _p(scale), _stream(stream)),
         "staple_quant_rows")
+
+
+def staple_matmul_i8(ctx, dtype, T, N, K, a, a_scale, b, b_scale, y, stream=None):
+    """y = (a b^T) a_scale b_scale with 8-bit a [T][K] and b [N][K] (see include/staple.h)."""
+    _ok(lib().staple_matmul_i8(ctx, dtype, T, N, K, _p(a), _p(a_scale), _p(b), _p(b_scale), _p(y),
+                               _stream(stream)), "staple_matmul_i8")

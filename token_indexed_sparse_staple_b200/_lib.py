@@ -81,6 +81,7 @@ SIGNATURES = {
     "staple_norm_bwd": (c_status, [vp, C.c_int, C.c_int, i32, i32, vp, vp, vp, vp, vp, vp,
                                    P(staple_drop), vp, vp, vp, vp, vp, sz, vp]),
     "staple_dropout": (c_status, [vp, C.c_int, i32, i32, vp, vp, P(staple_drop), vp, vp]),
+    "staple_matmul_i8": (c_status, [vp, C.c_int, i32, i32, i32, vp, vp, vp, vp, vp, vp]),
     "staple_quant_rows": (c_status, [vp, C.c_int, i32, i32, vp, vp, vp, vp]),
 }
 

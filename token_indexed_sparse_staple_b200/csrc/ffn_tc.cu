@@ -18,6 +18,7 @@
 #include "decode_fused.cuh"
 #include "gemm_tc.cuh"
 #include "internal.h"
+#include "tmap.h"
 
 namespace stp {
 
@@ -180,6 +181,20 @@ bool kmajor_rows(CUtensorMap* m, const void* base, int rows, int k, int64_t ld, 
 }
 
 }  // namespace
+
+bool tensor_map_2d(CUtensorMap* m, CUtensorMapDataType type, int esize, const void* base,
+                   uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_cols, uint32_t box_rows,
+                   CUtensorMapSwizzle swizzle) {
+  auto enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld * uint64_t(esize)};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // ---------------------------------------------------------------- decode
 namespace {

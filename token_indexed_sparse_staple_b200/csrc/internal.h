@@ -134,6 +134,13 @@ constexpr int kQuantMaxD = 32768;
 staple_status launch_quant_rows(const DeviceInfo& di, bool bf16, int T, int D, const void* x, int8_t* q, float* scale,
                                 cudaStream_t st);
 
+// matmul_i8.cu: K is at most kI8MaxK, so that no sum of products of two 8-bit
+// numbers leaves 32 bits (2^14 K < 2^31)
+constexpr int kI8MaxK = (1 << 17) - 16;
+staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, int K,
+                               const int8_t* a, const float* a_scale, const int8_t* b,
+                               const float* b_scale, void* y, int32_t* err, cudaStream_t st);
+
 // simt_f32.cu (fp32 on CUDA cores)
 staple_status f32_ffn_fwd(int T, int D, int F, const float* x, const staple_embed* e,
                           const float* wg, const float* wu, const float* wd, float* z, float* y,

@@ -1,0 +1,621 @@
+// Product of 8-bit integer matrices with a scale per token and per output
+// channel, on the tensor cores:
+//
+//   y[t][n] = float(sum_k a[t][k] b[n][k]) * a_scale[t] * b_scale[n]
+//
+// a [T][K] and b [N][K] are read in place by TMA (both K-major) into
+// 128-byte-swizzled shared-memory stages; tcgen05.mma.kind::i8 adds the
+// products up in int32, which is exact (K < 2^17, so a sum stays inside 32
+// bits), in tensor memory.  The epilogue rounds the sum to fp32, multiplies by
+// the two scales and rounds to the output type: three roundings of fp32 and
+// one of storage.
+//
+// Two kernels:
+//  * tiles: many tokens.  Tokens take the MMA's M side, 128 x 256 outputs per
+//    tile, persistent blocks, two accumulators in tensor memory so that a
+//    tile's epilogue runs beside the next tile's products.  Bound by the
+//    tensor cores.
+//  * split: few tiles (decode, or narrow outputs).  The weights take the M
+//    side (128 channels per tile) and up to 256 tokens the N side, so a block
+//    is a stream of weights; bound by HBM.  A tile's k range is split over the
+//    blocks of a cluster, which add their integer sums through distributed
+//    shared memory: no partial sums in memory, no counters, and integer adds
+//    give the same result in any order.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tmap.h"
+
+namespace stp {
+
+namespace {
+
+namespace i8 {
+
+constexpr int BK = 128;   // bytes (= k values) per 128-byte-swizzled row
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, signed 8-bit inputs, int32
+// accumulator; K = 32 per instruction.
+__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                     uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor for kind::i8: int32 accumulator, signed A and B, both
+// K-major.
+__host__ __device__ constexpr uint32_t idesc(int M, int N) {
+  return (2u << 4)                      // D format: s32
+         | (1u << 7)                    // A format: s8
+         | (1u << 10)                   // B format: s8
+         | (uint32_t(N >> 3) << 17)     // N / 8
+         | (uint32_t(M >> 4) << 24);    // M / 16
+}
+
+struct Params {
+  int32_t T, N, K;
+  const float* a_scale;
+  const float* b_scale;
+  void* y;
+  int32_t* err;
+  uint64_t wait_ns;
+  // tiles
+  int32_t tiles_t, tiles_n, group_t;
+  bool tma_out, vec_scale;
+  // split
+  int32_t tokens;        // tokens per tile, rounded up to 16 (the MMA's N)
+  int32_t cols;          // tensor-memory columns (a power of two >= 32)
+  int32_t stages, units; // 256-byte k units in all
+  int32_t cluster;
+  bool vec_out;
+};
+
+// ---------------------------------------------------------------- tiles
+
+constexpr int BM = 128, BN = 256, STAGES = 4, kThreads = 192;
+constexpr int A_STAGE = BM * BK, B_STAGE = BN * BK, STAGE_BYTES = A_STAGE + B_STAGE;
+constexpr int kOutBox = 32 * 32 * 4;    // one warp's staged 32 x 32 outputs (fp32 at most)
+// One block per SM, whatever the output type: two would not share the 512
+// columns of tensor memory, and the one that waits for them must not hold
+// shared memory that another kernel could use.
+constexpr int kTilesSmem = 226 * 1024;
+static_assert(1024 + STAGES * STAGE_BYTES + 4 * kOutBox + 256 <= kTilesSmem, "shared memory");
+
+__device__ __forceinline__ void tile_coords(int t, const Params& p, int& mb, int& nb) {
+  const int per_group = p.group_t * p.tiles_n;
+  const int g = t / per_group, first = g * p.group_t;
+  const int rows = min(p.group_t, p.tiles_t - first);
+  const int r = t - g * per_group;
+  mb = first + r % rows;
+  nb = r / rows;
+}
+
+// The 32 channel scales of columns n .. n + 31 (zero past N).
+__device__ __forceinline__ void load_scales(const Params& p, int n, float (&s)[32]) {
+  if (p.vec_scale && n + 32 <= p.N) {
+    const float4* q = reinterpret_cast<const float4*>(p.b_scale + n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = __ldg(q + i);
+      s[4 * i] = v.x; s[4 * i + 1] = v.y; s[4 * i + 2] = v.z; s[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = n + i < p.N ? __ldg(p.b_scale + n + i) : 0.0f;
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    tiles_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmO, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + STAGES * A_STAGE;
+  uint8_t* s_out = sB + STAGES * B_STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_out + 4 * kOutBox);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* dbar = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dbar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4);
+    }
+    mbar_init(dbar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int ntiles = p.tiles_t * p.tiles_n, kblocks = (p.K + BK - 1) / BK;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+        int mb, nb;
+        tile_coords(t, p, mb, nb);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+          tma_load_2d(&tmA, &full[stage], sA + stage * A_STAGE, kb * BK, mb * BM);
+          tma_load_2d(&tmB, &full[stage], sB + stage * B_STAGE, kb * BK, nb * BN);
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      drain_ring(full, STAGES, stage, phase, issued);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0, iter = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x, ++iter) {
+        const int buf = iter & 1;
+        if (!mbar_wait(&tempty[buf], (uint32_t(iter >> 1) & 1) ^ 1, abort_flag, p.err, p.wait_ns))
+          break;
+        tc_fence_after();
+        const uint32_t dacc = tmem_base + uint32_t(buf * BN);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(&full[stage], phase, abort_flag, p.err, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(sA + stage * A_STAGE), b = smem_u32(sB + stage * B_STAGE);
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            umma(dacc, sw128_desc(a + k * 32, 16, 1024), sw128_desc(b + k * 32, 16, 1024),
+                 idesc(BM, BN), (kb | k) ? 1u : 0u);
+          umma_commit(&empty[stage]);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) umma_commit(&tfull[buf]);
+      }
+      umma_commit(dbar);
+      mbar_drain(dbar, 0);
+    }
+  } else {
+    const int q = warp & 3;
+    uint8_t* stg = s_out + q * kOutBox;
+    int iter = 0;
+    for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++iter) {
+      const int buf = iter & 1;
+      int mb, nb;
+      tile_coords(t, p, mb, nb);
+      const int m0 = mb * BM + q * 32, m = m0 + lane;
+      const float sa = m < p.T ? __ldg(p.a_scale + m) : 0.0f;
+      const bool ok = mbar_wait(&tfull[buf], uint32_t(iter >> 1) & 1, abort_flag, p.err, p.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(buf * BN);
+#pragma unroll 1
+      for (int c = 0; c < BN / 32; ++c) {
+        const int n = nb * BN + c * 32;
+        if (n >= p.N) break;          // the same for the whole warp
+        float sb[32];
+        load_scales(p, n, sb);
+        uint32_t r[32];
+        tmem_ld32(tacc + c * 32, r);
+        tmem_ld_wait(r);
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = float(int(r[i])) * sa * sb[i];
+        // stage the 32 x 32 block, swizzled as the TMA store expects it (and
+        // free of bank conflicts either way)
+        if (p.tma_out) {
+          if (lane == 0) bulk_wait_read0();
+        }
+        __syncwarp();
+        if constexpr (BF16) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pack_bf2(v[8 * k], v[8 * k + 1]), pack_bf2(v[8 * k + 2], v[8 * k + 3]),
+                           pack_bf2(v[8 * k + 4], v[8 * k + 5]),
+                           pack_bf2(v[8 * k + 6], v[8 * k + 7]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<float4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+        if (p.tma_out) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmO, stg, n, m0);
+            bulk_commit();
+          }
+        } else {
+          // rows that TMA cannot address (pitch not a multiple of 16 bytes):
+          // one row at a time, a warp's 32 columns side by side
+          __syncwarp();
+          const int rows = min(32, p.T - m0);
+          if (n + lane < p.N)
+            for (int i = 0; i < rows; ++i) {
+              const int64_t o = int64_t(m0 + i) * p.N + n + lane;
+              if constexpr (BF16)
+                static_cast<uint16_t*>(p.y)[o] = *reinterpret_cast<const uint16_t*>(
+                    stg + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2);
+              else
+                static_cast<float*>(p.y)[o] = *reinterpret_cast<const float*>(
+                    stg + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4);
+            }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[buf]);
+    }
+    if (p.tma_out && lane == 0) bulk_wait0();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------- split
+
+constexpr int kUnit = 2 * BK;               // 256 bytes of each weight row per stage
+constexpr int kWStage = BM * kUnit;         // 32 KiB of weights
+constexpr int kMaxTokens = 256, kMaxCluster = 8, kMaxStages = 12;
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
+                   "memory");
+}
+__device__ __forceinline__ int4 ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  int4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// Four channels n .. n + 3 of one token.
+template <bool BF16>
+__device__ __forceinline__ void store4(const Params& p, int t, int n, const float (&v)[4]) {
+  const int64_t o = int64_t(t) * p.N + n;
+  if (p.vec_out && n + 4 <= p.N) {
+    if constexpr (BF16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + o) =
+          make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(p.y) + o) =
+          make_float4(v[0], v[1], v[2], v[3]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < p.N) {
+      if constexpr (BF16)
+        static_cast<uint16_t*>(p.y)[o + i] = uint16_t(pack_bf2(v[i], 0.0f) & 0xffffu);
+      else
+        static_cast<float*>(p.y)[o + i] = v[i];
+    }
+}
+
+// Block = 6 warps: 0 loads, 1 MMAs, 2..5 drain the accumulator.  blockIdx.x =
+// tile * cluster + rank; blockIdx.y = token tile.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads)
+    split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                 const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_i;
+  volatile int* abort_flag = &abort_i;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int C = p.cluster, rank = blockIdx.x % C, n0 = (blockIdx.x / C) * BM;
+  const int t0 = blockIdx.y * kMaxTokens;
+  const int S = p.stages, x_bytes = p.tokens * BK;        // one 128-byte k block of tokens
+  const int stage_bytes = kWStage + 2 * x_bytes;
+  // this block's k units
+  const int u0 = int(int64_t(p.units) * rank / C), u1 = int(int64_t(p.units) * (rank + 1) / C);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&tfull, 1);
+    abort_i = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, p.cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  if (warp == 0) {
+    if (lane == 0) {
+      // weights that no other token tile reads need not stay in L2
+      const bool once = gridDim.y == 1;
+      const uint64_t policy = l2_policy_evict_first();
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      for (int u = u0; u < u1; ++u) {
+        if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, p.wait_ns)) break;
+        uint8_t* w = smem + stage * stage_bytes;
+        uint8_t* x = w + kWStage;
+        mbar_arrive_expect_tx(&full[stage], stage_bytes);
+        for (int h = 0; h < 2; ++h) {
+          const int k = u * kUnit + h * BK;     // past K: zeros
+          if (once)
+            tma_load_2d_hint(&tmW, &full[stage], w + h * (kWStage / 2), k, n0, policy);
+          else
+            tma_load_2d(&tmW, &full[stage], w + h * (kWStage / 2), k, n0);
+          tma_load_2d(&tmX, &full[stage], x + h * x_bytes, k, t0);
+        }
+        ++issued;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      drain_ring(full, S, stage, phase, issued);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id = idesc(BM, p.tokens);
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int u = u0; u < u1; ++u) {
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.err, p.wait_ns)) break;
+        tc_fence_after();
+        const uint32_t w = smem_u32(smem + stage * stage_bytes), x = w + kWStage;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          umma(tmem_base,
+               sw128_desc(w + (k >> 2) * (kWStage / 2) + (k & 3) * 32, 16, 1024),
+               sw128_desc(x + (k >> 2) * x_bytes + (k & 3) * 32, 16, 1024), id,
+               (u != u0 || k) ? 1u : 0u);
+        umma_commit(&empty[stage]);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      umma_commit(&tfull);
+    }
+  }
+  __syncwarp();
+  // every product of this block is in tensor memory, and its stages are free
+  mbar_wait(&tfull, 0, abort_flag, p.err, p.wait_ns);
+  if (*abort_flag && warp == 1 && lane == 0) mbar_drain(&tfull, 0);
+  __syncthreads();
+  tc_fence_after();
+  const int tokens = min(p.tokens, p.T - t0);
+  int32_t* acc = reinterpret_cast<int32_t*>(smem);        // [tokens][128]
+  if (warp >= 2) {
+    // thread = channel, registers = tokens
+    const int q = warp & 3;
+    const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16);
+    for (int c = 0; c < p.tokens; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(tacc + c, r);
+      tmem_ld_wait16(r);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[(c + i) * BM + q * 32 + lane] = int(r[i]);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem_base, p.cols);
+  }
+  if (C > 1) cluster_sync();
+  // tokens rank, rank + C, ... of the tile: one warp per token, four channels
+  // per lane, the blocks' sums added
+  const int n = n0 + lane * 4;
+  float sb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sb[i] = n + i < p.N ? __ldg(p.b_scale + n + i) : 0.0f;
+  for (int t = rank + C * warp; t < tokens; t += C * (kThreads / 32)) {
+    const uint32_t at = smem_u32(acc + t * BM + lane * 4);
+    int4 s = make_int4(0, 0, 0, 0);
+    if (C == 1) {
+      s = *reinterpret_cast<const int4*>(acc + t * BM + lane * 4);
+    } else {
+#pragma unroll 4
+      for (int r = 0; r < C; ++r) {
+        const int4 v = ld_cluster(at, uint32_t(r));
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+    }
+    const float sa = __ldg(p.a_scale + t0 + t);
+    const float v[4] = {float(s.x) * sa * sb[0], float(s.y) * sa * sb[1], float(s.z) * sa * sb[2],
+                        float(s.w) * sa * sb[3]};
+    store4<BF16>(p, t0 + t, n, v);
+  }
+  if (C > 1) cluster_sync();   // the sums stay until every block has read them
+}
+
+inline int cdiv(int64_t a, int64_t b) { return int((a + b - 1) / b); }
+
+}  // namespace i8
+
+// Shared memory of a split block.  Blocks that share an SM share its 512
+// columns of tensor memory, and a block that waits for columns could wait for
+// a cluster whose other blocks wait for it: so no block takes a smaller part
+// of the SM's 228 KB than of its columns, and none fits beside a tiled GEMM
+// block (at least 193.25 KB and all columns).
+int split_smem(int stages, int stage_bytes, int tokens, int cols) {
+  const int want = std::max(stages * stage_bytes, tokens * i8::BM * 4) + 1024;
+  const int share = int(int64_t(cols) * 228 * 1024 / 512) - 1024;
+  return std::max(std::max(want, share), 36 * 1024);
+}
+
+template <typename K>
+bool opt_in(K kern, int bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = uint64_t(1) << (device & 63);
+  if (done.load() & bit) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return false;
+  done.fetch_or(bit);
+  return true;
+}
+
+template <bool BF16>
+staple_status go_tiles(const DeviceInfo& di, const CUtensorMap& a, const CUtensorMap& b,
+                       const CUtensorMap& o, const i8::Params& p, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto kern = i8::tiles_kernel<BF16>;
+  if (!opt_in(kern, i8::kTilesSmem, di.device, done)) return STAPLE_ECUDA;
+  const int ntiles = p.tiles_t * p.tiles_n;
+  const int avail = std::max(1, di.num_sms - di.sm_reserve);
+  const int per = i8::cdiv(ntiles, avail);
+  STP_LAUNCH("matmul_i8", st,
+             kern<<<i8::cdiv(ntiles, per), i8::kThreads, i8::kTilesSmem, st>>>(a, b, o, p));
+  return cudaGetLastError() == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+}
+
+template <bool BF16>
+staple_status go_split(const DeviceInfo& di, const CUtensorMap& w, const CUtensorMap& x,
+                       const i8::Params& p, int tiles_n, int tiles_t, int smem, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto kern = i8::split_kernel<BF16>;
+  if (!opt_in(kern, 226 * 1024, di.device, done)) return STAPLE_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(tiles_n) * unsigned(p.cluster), unsigned(tiles_t));
+  cfg.blockDim = dim3(i8::kThreads);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(p.cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t ce = cudaSuccess;
+  STP_LAUNCH("matmul_i8_split", st, ce = cudaLaunchKernelEx(&cfg, kern, w, x, p));
+  return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+}
+
+}  // namespace
+
+staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, int K,
+                               const int8_t* a, const float* a_scale, const int8_t* b,
+                               const float* b_scale, void* y, int32_t* err, cudaStream_t st) {
+  if (T == 0) return STAPLE_OK;
+  // tiles are counted in 32 bits
+  if (int64_t(i8::cdiv(T, i8::BM)) * i8::cdiv(N, i8::BN) > INT32_MAX / 2) return STAPLE_EUNSUPPORTED;
+  const int es = bf16 ? 2 : 4;
+  i8::Params p{};
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.a_scale = a_scale;
+  p.b_scale = b_scale;
+  p.y = y;
+  p.err = err;
+  p.wait_ns = di.wait_ns;
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  CUtensorMap ma, mb, mo;
+  p.tiles_t = i8::cdiv(T, i8::BM);
+  p.tiles_n = i8::cdiv(N, i8::BN);
+  if (T > i8::kMaxTokens && int64_t(p.tiles_t) * p.tiles_n >= di.num_sms) {
+    p.group_t = 16;
+    p.vec_scale = (reinterpret_cast<uintptr_t>(b_scale) & 15u) == 0;
+    p.tma_out = (int64_t(N) * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
+    if (!tensor_map_2d(&ma, u8, 1, a, K, T, K, i8::BK, i8::BM, sw) ||
+        !tensor_map_2d(&mb, u8, 1, b, K, N, K, i8::BK, i8::BN, sw))
+      return STAPLE_ECUDA;
+    mo = ma;
+    if (p.tma_out &&
+        !tensor_map_2d(&mo, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                       es, y, N, T, N, 32, 32,
+                       bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+      return STAPLE_ECUDA;
+    return bf16 ? go_tiles<true>(di, ma, mb, mo, p, st) : go_tiles<false>(di, ma, mb, mo, p, st);
+  }
+  const int tiles_n = i8::cdiv(N, i8::BM), tiles_t = i8::cdiv(T, i8::kMaxTokens);
+  p.tokens = std::min(i8::kMaxTokens, i8::cdiv(T, 16) * 16);
+  p.cols = 32;
+  while (p.cols < p.tokens) p.cols <<= 1;
+  p.units = i8::cdiv(K, i8::kUnit);
+  p.vec_out = (N % 4) == 0 && (reinterpret_cast<uintptr_t>(y) & uintptr_t(4 * es - 1)) == 0;
+  const int stage_bytes = i8::kWStage + 2 * p.tokens * i8::BK;
+  // The cluster size with the least work on the fullest SM, in k units; a sum
+  // over a cluster costs about as much as four.
+  int best = INT32_MAX, smem = 0;
+  for (int c = 1; c <= i8::kMaxCluster && c <= p.units; ++c) {
+    const int per_sm = i8::cdiv(int64_t(tiles_n) * tiles_t * c, di.num_sms);
+    const int per_block = i8::cdiv(p.units, c);
+    const int cost = per_sm * per_block + (c > 1 ? 4 : 0);
+    if (cost >= best) continue;
+    // as many blocks per SM as there are, if each gets two stages
+    int fit = std::min(per_sm, 512 / p.cols), stages = 0;
+    for (; fit >= 1; --fit) {
+      const int avail = std::min(228 * 1024 / fit - 2048, 225 * 1024) - 1024;
+      stages = std::min(std::min(per_block, i8::kMaxStages), avail / stage_bytes);
+      if (stages >= std::min(2, per_block)) break;
+    }
+    if (fit < 1) continue;
+    best = cost;
+    p.cluster = c;
+    p.stages = stages;
+    smem = split_smem(stages, stage_bytes, p.tokens, p.cols);
+  }
+  if (!tensor_map_2d(&mb, u8, 1, b, K, N, K, i8::BK, i8::BM, sw) ||
+      !tensor_map_2d(&ma, u8, 1, a, K, T, K, i8::BK, uint32_t(p.tokens), sw))
+    return STAPLE_ECUDA;
+  return bf16 ? go_split<true>(di, mb, ma, p, tiles_n, tiles_t, smem, st)
+              : go_split<false>(di, mb, ma, p, tiles_n, tiles_t, smem, st);
+}
+
+}  // namespace stp

@@ -820,4 +820,22 @@ staple_status staple_quant_rows(staple_context* ctx, staple_dtype dtype, int32_t
   return stp::launch_quant_rows(ctx->di, dtype == STAPLE_BF16, T, D, x, q, scale, cs(stream));
 }
 
+staple_status staple_matmul_i8(staple_context* ctx, staple_dtype dtype, int32_t T, int32_t N,
+                               int32_t K, const int8_t* a, const float* a_scale, const int8_t* b,
+                               const float* b_scale, void* y, staple_stream stream) {
+  if (!ctx) return STAPLE_EINVAL;
+  STP_TRY(check_rows(dtype, T, N));
+  if (K <= 0 || K % 16) return STAPLE_EINVAL;
+  if (K > stp::kI8MaxK) return STAPLE_EUNSUPPORTED;
+  if (T == 0) return STAPLE_OK;
+  if (!a || !b || !aligned16(a) || !aligned16(b)) return STAPLE_EINVAL;
+  if (!a_scale || !b_scale || !aligned_to(a_scale, 4) || !aligned_to(b_scale, 4))
+    return STAPLE_EINVAL;
+  if (!rows_ok(dtype, {y}, {})) return STAPLE_EINVAL;
+  STP_TRY(set_device(ctx));
+  stp::TraceScope trace_scope(ctx->tracer);
+  return stp::launch_matmul_i8(ctx->di, dtype == STAPLE_BF16, T, N, K, a, a_scale, b, b_scale, y,
+                               ctx->d_err, cs(stream));
+}
+
 }  // extern "C"
