@@ -33,6 +33,14 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
+// Wait until the kernels before this one in the stream have completed and
+// their writes are visible.  A kernel launched as a programmatic dependent may
+// start while the one before it drains; everything it reads from memory, and
+// everything it writes, comes after this.
+__device__ __forceinline__ void wait_prior_kernels() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // bf16 <-> fp32
 // ---------------------------------------------------------------------------

@@ -43,6 +43,30 @@ struct TraceScope {                                   // makes a tracer current 
     ::stp::trace_end(_slot, st);                      \
   } while (0)
 
+// Launch a kernel as a programmatic dependent of what is before it in the
+// stream: its blocks start, and set up what needs no memory, while the kernel
+// before drains.  The kernel calls wait_prior_kernels() before it touches
+// memory.  cluster: blocks per cluster along x.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned block, size_t smem,
+                                    cudaStream_t st, unsigned cluster, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // retrieval.cu
 staple_status launch_dedup(const int32_t* ids, int T, int64_t V, int32_t* unique,
                            int32_t* inverse, int32_t* seg_off, int32_t* sorted_pos,

@@ -16,11 +16,10 @@
 //    tile's epilogue runs beside the next tile's products.  Bound by the
 //    tensor cores.
 //  * split: few tiles (decode, or narrow outputs).  The weights take the M
-//    side (128 channels per tile) and up to 256 tokens the N side, so a block
-//    is a stream of weights; bound by HBM.  A tile's k range is split over the
-//    blocks of a cluster, which add their integer sums through distributed
-//    shared memory: no partial sums in memory, no counters, and integer adds
-//    give the same result in any order.
+//    side and up to 256 tokens the N side, so a block is a stream of weights;
+//    bound by HBM.  Where k is split too, the blocks of a cluster add their
+//    integer sums through distributed shared memory: no partial sums in
+//    memory, no counters, and integer adds give the same result in any order.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -38,15 +37,27 @@ namespace i8 {
 
 constexpr int BK = 128;   // bytes (= k values) per 128-byte-swizzled row
 
+// One lane of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n"
+               : "=r"(p));
+  return p;
+}
+
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, signed 8-bit inputs, int32
-// accumulator; K = 32 per instruction.
+// accumulator; K = 32 per instruction.  The whole warp calls it with the same
+// operands and the elected lane issues it: a loop that only one lane runs
+// moves every operand into the uniform registers anew, which took 100 cycles
+// per instruction here, more than a 128 x 64 x 32 product takes (49).
 __device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                     uint32_t idesc, uint32_t accumulate) {
+                                     uint32_t idesc, uint32_t accumulate, uint32_t elected) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
 
@@ -73,8 +84,8 @@ struct Params {
   // split
   int32_t tokens;        // tokens per tile, rounded up to 16 (the MMA's N)
   int32_t cols;          // tensor-memory columns (a power of two >= 32)
+  int32_t rows;          // channels per tile, a multiple of 8 up to 128
   int32_t stages, units; // 256-byte k units in all
-  int32_t cluster;
   bool vec_out;
 };
 
@@ -181,38 +192,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_ring(full, STAGES, stage, phase, issued);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0, iter = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x, ++iter) {
-        const int buf = iter & 1;
-        if (!mbar_wait(&tempty[buf], (uint32_t(iter >> 1) & 1) ^ 1, abort_flag, p.err, p.wait_ns))
+    const uint32_t elected = elect_one();
+    const uint64_t a0 = sw128_desc(smem_u32(sA), 16, 1024), b0 = sw128_desc(smem_u32(sB), 16, 1024);
+    int stage = 0, iter = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x, ++iter) {
+      const int buf = iter & 1;
+      ok = mbar_wait(&tempty[buf], (uint32_t(iter >> 1) & 1) ^ 1, abort_flag, p.err, p.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t dacc = tmem_base + uint32_t(buf * BN);
+      for (int kb = 0; kb < kblocks; ++kb) {
+        ok = mbar_wait(&full[stage], phase, abort_flag, p.err, p.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
           break;
-        tc_fence_after();
-        const uint32_t dacc = tmem_base + uint32_t(buf * BN);
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, p.err, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a = smem_u32(sA + stage * A_STAGE), b = smem_u32(sB + stage * B_STAGE);
-#pragma unroll
-          for (int k = 0; k < BK / 32; ++k)
-            umma(dacc, sw128_desc(a + k * 32, 16, 1024), sw128_desc(b + k * 32, 16, 1024),
-                 idesc(BM, BN), (kb | k) ? 1u : 0u);
-          umma_commit(&empty[stage]);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
         }
-        if (ok) umma_commit(&tfull[buf]);
+        tc_fence_after();
+        const uint64_t a = a0 + uint64_t(stage * (A_STAGE >> 4));
+        const uint64_t b = b0 + uint64_t(stage * (B_STAGE >> 4));
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k)   // 32 bytes further on: 2 in the address field
+          umma(dacc, a + 2 * k, b + 2 * k, idesc(BM, BN), (kb | k) ? 1u : 0u, elected);
+        if (elected) umma_commit(&empty[stage]);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
-      umma_commit(dbar);
-      mbar_drain(dbar, 0);
+      if (ok && elected) umma_commit(&tfull[buf]);
     }
+    if (elected) umma_commit(dbar);
+    __syncwarp();
+    mbar_drain(dbar, 0);
   } else {
     const int q = warp & 3;
     uint8_t* stg = s_out + q * kOutBox;
@@ -299,9 +312,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- split
 
-constexpr int kUnit = 2 * BK;               // 256 bytes of each weight row per stage
-constexpr int kWStage = BM * kUnit;         // 32 KiB of weights
-constexpr int kMaxTokens = 256, kMaxCluster = 8, kMaxStages = 12;
+// The bound is HBM, so the tiles are cut to keep every SM streaming: a tile is
+// `rows` channels high, not 128 (the MMA's M stays 128; what it computes of
+// the rows that no copy wrote is not read), and the height is chosen so that
+// the tiles are as many as the SMs.  Only outputs too narrow for that, or with
+// so many tokens that their re-reading from L2 would cost more, split k too.
+constexpr int kUnit = 2 * BK;               // 256 bytes of each row per stage
+constexpr int kMaxTokens = 256, kMaxStages = 24;
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
@@ -313,16 +330,16 @@ __device__ __forceinline__ int4 ld_cluster(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
+               : "r"(a));
   return v;
 }
 
-// Four channels n .. n + 3 of one token.
+// Channels n .. n + 3 of one token, of which `left` are this tile's.
 template <bool BF16>
-__device__ __forceinline__ void store4(const Params& p, int t, int n, const float (&v)[4]) {
+__device__ __forceinline__ void store4(const Params& p, int t, int n, int left,
+                                       const float (&v)[4]) {
   const int64_t o = int64_t(t) * p.N + n;
-  if (p.vec_out && n + 4 <= p.N) {
+  if (p.vec_out && left >= 4) {
     if constexpr (BF16)
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + o) =
           make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
@@ -333,7 +350,7 @@ __device__ __forceinline__ void store4(const Params& p, int t, int n, const floa
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (n + i < p.N) {
+    if (i < left) {
       if constexpr (BF16)
         static_cast<uint16_t*>(p.y)[o + i] = uint16_t(pack_bf2(v[i], 0.0f) & 0xffffu);
       else
@@ -342,8 +359,8 @@ __device__ __forceinline__ void store4(const Params& p, int t, int n, const floa
 }
 
 // Block = 6 warps: 0 loads, 1 MMAs, 2..5 drain the accumulator.  blockIdx.x =
-// tile * cluster + rank; blockIdx.y = token tile.
-template <bool BF16>
+// tile * C + rank in the cluster; blockIdx.y = token tile.
+template <bool BF16, int C>
 __global__ void __launch_bounds__(kThreads)
     split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                  const Params p) {
@@ -352,150 +369,257 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_i;
+  __shared__ float s_scale[kMaxTokens];
   volatile int* abort_flag = &abort_i;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int C = p.cluster, rank = blockIdx.x % C, n0 = (blockIdx.x / C) * BM;
-  const int t0 = blockIdx.y * kMaxTokens;
-  const int S = p.stages, x_bytes = p.tokens * BK;        // one 128-byte k block of tokens
-  const int stage_bytes = kWStage + 2 * x_bytes;
+  if (threadIdx.x == 0) {          // the maps' way into the cache is the longest: first
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+  }
+  const uint32_t rank = blockIdx.x % C;
+  const int n0 = int(blockIdx.x / C) * p.rows, t0 = int(blockIdx.y) * kMaxTokens;
+  const int S = p.stages;
+  // a k block of 128 bytes: weights, tokens (the tokens' tiles start on 1 KB
+  // boundaries as both are multiples of eight rows)
+  const int w_bytes = p.rows * BK, x_bytes = p.tokens * BK;
+  const int stage_bytes = 2 * (w_bytes + x_bytes);
   // this block's k units
-  const int u0 = int(int64_t(p.units) * rank / C), u1 = int(int64_t(p.units) * (rank + 1) / C);
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+  const int u0 = p.units * int(rank) / C, u1 = p.units * (int(rank) + 1) / C;
+  const int len = u1 - u0, first = min(S, len);   // units, fills of the first lap
+  // Tiles start at different units of k (the sum does not mind): in step, all
+  // blocks would read the same tokens' lines from L2 at the same time.
+  const int shift = int(blockIdx.x / C) % len;
+  auto unit = [&](int i) { return u0 + (i + shift < len ? i + shift : i + shift - len); };
+  const uint64_t policy = l2_policy_evict_first();
+  auto load_w = [&](int i, int stage) {
+    uint8_t* w = smem + stage * stage_bytes;
+    for (int h = 0; h < 2; ++h) {
+      const int k = unit(i) * kUnit + h * BK;     // past K: zeros
+      // weights that no other token tile reads need not stay in L2
+      if (gridDim.y == 1)
+        tma_load_2d_hint(&tmW, &full[stage], w + h * w_bytes, k, n0, policy);
+      else
+        tma_load_2d(&tmW, &full[stage], w + h * w_bytes, k, n0);
     }
-    mbar_init(&tfull, 1);
-    abort_i = 0;
+  };
+  auto load_x = [&](int i, int stage) {
+    uint8_t* x = smem + stage * stage_bytes + 2 * w_bytes;
+    for (int h = 0; h < 2; ++h)
+      tma_load_2d(&tmX, &full[stage], x + h * x_bytes, unit(i) * kUnit + h * BK, t0);
+  };
+  // Warp 0 sets the barriers up and sends the first ring of loads out before
+  // the block's set-up barrier.
+  if (warp == 0) {
+    if (lane < S) {
+      mbar_init(&full[lane], 1);
+      mbar_init(&empty[lane], 1);
+    }
+    if (lane == 0) {
+      mbar_init(&tfull, 1);
+      abort_i = 0;
+    }
     fence_barrier_init();
+    if (lane < first) mbar_arrive_expect_tx(&full[lane], stage_bytes);
+    wait_prior_kernels();
+    __syncwarp();
+    if (lane == 0)
+      for (int s = 0; s < first; ++s) {
+        load_w(s, s);
+        load_x(s, s);
+      }
+    __syncwarp();
   }
   if (warp == 1) {
     tmem_alloc(&tmem_slot, p.cols);
     tmem_relinquish();
   }
+  if (warp != 0) wait_prior_kernels();
+  const int tokens = min(p.tokens, p.T - t0);
+  const int channels = min(p.rows, p.N - n0);
+  // The scales are fetched now: at the end their latency would count.  One
+  // block: a thread has one channel; a cluster: four (see the sums below).
+  const int row = (warp & 3) * 32 + lane;   // this thread's accumulator row (warps 2..5)
+  float sb[C == 1 ? 1 : 4];
+  if constexpr (C == 1) {
+    sb[0] = row < channels ? __ldg(p.b_scale + n0 + row) : 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sb[i] = lane * 4 + i < channels ? __ldg(p.b_scale + n0 + lane * 4 + i) : 0.0f;
+  }
+  if (warp >= 2)
+    for (int t = threadIdx.x - 64; t < tokens; t += kThreads - 64)
+      s_scale[t] = __ldg(p.a_scale + t0 + t);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
   if (warp == 0) {
     if (lane == 0) {
-      // weights that no other token tile reads need not stay in L2
-      const bool once = gridDim.y == 1;
-      const uint64_t policy = l2_policy_evict_first();
-      int stage = 0, issued = 0;
+      int stage = 0, issued = first;
       uint32_t phase = 0;
-      for (int u = u0; u < u1; ++u) {
-        if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, p.wait_ns)) break;
-        uint8_t* w = smem + stage * stage_bytes;
-        uint8_t* x = w + kWStage;
+      for (; issued < len; ++issued) {
+        if (!mbar_wait(&empty[stage], phase, abort_flag, p.err, p.wait_ns)) break;
         mbar_arrive_expect_tx(&full[stage], stage_bytes);
-        for (int h = 0; h < 2; ++h) {
-          const int k = u * kUnit + h * BK;     // past K: zeros
-          if (once)
-            tma_load_2d_hint(&tmW, &full[stage], w + h * (kWStage / 2), k, n0, policy);
-          else
-            tma_load_2d(&tmW, &full[stage], w + h * (kWStage / 2), k, n0);
-          tma_load_2d(&tmX, &full[stage], x + h * x_bytes, k, t0);
-        }
-        ++issued;
+        load_w(issued, stage);
+        load_x(issued, stage);
         if (++stage == S) {
           stage = 0;
           phase ^= 1;
         }
       }
-      drain_ring(full, S, stage, phase, issued);
+      drain_ring(full, S, issued % S, uint32_t(issued / S) & 1, issued);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id = idesc(BM, p.tokens);
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int u = u0; u < u1; ++u) {
-        if (!mbar_wait(&full[stage], phase, abort_flag, p.err, p.wait_ns)) break;
-        tc_fence_after();
-        const uint32_t w = smem_u32(smem + stage * stage_bytes), x = w + kWStage;
+    const uint32_t id = idesc(BM, p.tokens), elected = elect_one();
+    const uint64_t d0 = sw128_desc(smem_u32(smem), 16, 1024);
+    const uint32_t dw = uint32_t(w_bytes) >> 4, dx = uint32_t(x_bytes) >> 4;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < len; ++i) {
+      const bool ok = mbar_wait(&full[stage], phase, abort_flag, p.err, p.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint64_t w = d0 + uint64_t(uint32_t(stage * stage_bytes) >> 4), x = w + 2 * dw;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma(tmem_base,
-               sw128_desc(w + (k >> 2) * (kWStage / 2) + (k & 3) * 32, 16, 1024),
-               sw128_desc(x + (k >> 2) * x_bytes + (k & 3) * 32, 16, 1024), id,
-               (u != u0 || k) ? 1u : 0u);
-        umma_commit(&empty[stage]);
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1;
-        }
+      for (int k = 0; k < 8; ++k)   // 32 bytes further on: 2 in the address field
+        umma(tmem_base, w + (k >> 2) * dw + (k & 3) * 2, x + (k >> 2) * dx + (k & 3) * 2, id,
+             (i | k) ? 1u : 0u, elected);
+      if (elected) umma_commit(&empty[stage]);
+      if (++stage == S) {
+        stage = 0;
+        phase ^= 1;
       }
-      umma_commit(&tfull);
     }
+    if (elected) umma_commit(&tfull);
   }
   __syncwarp();
   // every product of this block is in tensor memory, and its stages are free
   mbar_wait(&tfull, 0, abort_flag, p.err, p.wait_ns);
-  if (*abort_flag && warp == 1 && lane == 0) mbar_drain(&tfull, 0);
-  __syncthreads();
+  if (*abort_flag && warp == 1) mbar_drain(&tfull, 0);
+  __syncwarp();
   tc_fence_after();
-  const int tokens = min(p.tokens, p.T - t0);
-  int32_t* acc = reinterpret_cast<int32_t*>(smem);        // [tokens][128]
-  if (warp >= 2) {
-    // thread = channel, registers = tokens
-    const int q = warp & 3;
-    const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16);
-    for (int c = 0; c < p.tokens; c += 16) {
-      uint32_t r[16];
-      tmem_ld16(tacc + c, r);
-      tmem_ld_wait16(r);
+  const uint32_t tacc = tmem_base + (uint32_t((warp & 3) * 32) << 16);
+  if constexpr (C == 1) {
+    // thread = channel: a warp writes 32 neighbouring channels of one token
+    if (warp >= 2 && (warp & 3) * 32 < channels) {
+      const size_t es = BF16 ? 2 : 4, pitch = size_t(p.N) * es;
+      uint8_t* y = static_cast<uint8_t*>(p.y) + size_t(t0) * pitch + size_t(n0 + row) * es;
+      const bool row_ok = row < channels;
+      for (int c = 0; c < tokens; c += 16, y += 16 * pitch) {
+        uint32_t r[16];
+        tmem_ld16(tacc + c, r);
+        tmem_ld_wait16(r);
+        const int n = row_ok ? tokens - c : 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[(c + i) * BM + q * 32 + lane] = int(r[i]);
-    }
-    tc_fence_before();
-  }
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) {
-    __syncwarp();
-    tmem_dealloc(tmem_base, p.cols);
-  }
-  if (C > 1) cluster_sync();
-  // tokens rank, rank + C, ... of the tile: one warp per token, four channels
-  // per lane, the blocks' sums added
-  const int n = n0 + lane * 4;
-  float sb[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) sb[i] = n + i < p.N ? __ldg(p.b_scale + n + i) : 0.0f;
-  for (int t = rank + C * warp; t < tokens; t += C * (kThreads / 32)) {
-    const uint32_t at = smem_u32(acc + t * BM + lane * 4);
-    int4 s = make_int4(0, 0, 0, 0);
-    if (C == 1) {
-      s = *reinterpret_cast<const int4*>(acc + t * BM + lane * 4);
-    } else {
-#pragma unroll 4
-      for (int r = 0; r < C; ++r) {
-        const int4 v = ld_cluster(at, uint32_t(r));
-        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        for (int i = 0; i < 16; ++i) {
+          const float v = float(int(r[i])) * s_scale[c + i] * sb[0];
+          if (i < n) {
+            if constexpr (BF16)
+              *reinterpret_cast<uint16_t*>(y + i * pitch) = uint16_t(pack_bf2(v, 0.0f) & 0xffffu);
+            else
+              *reinterpret_cast<float*>(y + i * pitch) = v;
+          }
+        }
       }
     }
-    const float sa = __ldg(p.a_scale + t0 + t);
-    const float v[4] = {float(s.x) * sa * sb[0], float(s.y) * sa * sb[1], float(s.z) * sa * sb[2],
-                        float(s.w) * sa * sb[3]};
-    store4<BF16>(p, t0 + t, n, v);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, p.cols);
+  } else {
+    __syncthreads();     // a stage may be written once nothing can still fill or read it
+    int32_t* acc = reinterpret_cast<int32_t*>(smem);        // [tokens][128]
+    if (warp >= 2) {
+      for (int c = 0; c < p.tokens; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(tacc + c, r);
+        tmem_ld_wait16(r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[(c + i) * BM + row] = int(r[i]);
+      }
+      tc_fence_before();
+    }
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, p.cols);
+    // tokens rank, rank + C, ... of the tile: one warp per token, four
+    // channels per lane, the blocks' sums added
+    const int n = n0 + lane * 4;
+#pragma unroll 2
+    for (int t = int(rank) + C * warp; t < tokens; t += C * (kThreads / 32)) {
+      const uint32_t at = smem_u32(acc + t * BM + lane * 4);
+      int4 v[C];
+      v[0] = *reinterpret_cast<const int4*>(acc + t * BM + lane * 4);
+#pragma unroll
+      for (int r = 1; r < C; ++r) v[r] = ld_cluster(at, (rank + r) % C);
+#pragma unroll
+      for (int r = 1; r < C; ++r) {
+        v[0].x += v[r].x; v[0].y += v[r].y; v[0].z += v[r].z; v[0].w += v[r].w;
+      }
+      const float sa = s_scale[t];
+      const float f[4] = {float(v[0].x) * sa * sb[0], float(v[0].y) * sa * sb[1],
+                          float(v[0].z) * sa * sb[2], float(v[0].w) * sa * sb[3]};
+      store4<BF16>(p, t0 + t, n, channels - lane * 4, f);
+    }
+    cluster_sync();   // the sums stay until every block has read them
   }
-  if (C > 1) cluster_sync();   // the sums stay until every block has read them
 }
 
 inline int cdiv(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 
 }  // namespace i8
 
-// Shared memory of a split block.  Blocks that share an SM share its 512
-// columns of tensor memory, and a block that waits for columns could wait for
-// a cluster whose other blocks wait for it: so no block takes a smaller part
-// of the SM's 228 KB than of its columns, and none fits beside a tiled GEMM
-// block (at least 193.25 KB and all columns).
-int split_smem(int stages, int stage_bytes, int tokens, int cols) {
-  const int want = std::max(stages * stage_bytes, tokens * i8::BM * 4) + 1024;
-  const int share = int(int64_t(cols) * 228 * 1024 / 512) - 1024;
-  return std::max(std::max(want, share), 36 * 1024);
+// How a few-tiles product is cut.
+struct SplitPlan {
+  int cluster, rows, stages, smem;
+};
+
+constexpr int kSplitSmemMax = 225 * 1024;   // beside 1.5 KB of static arrays
+
+// Every candidate cluster size with the tile height that fills the SMs (w
+// blocks each), and the estimated time on one SM in us: its share of the
+// weights at its share of HBM (43.6 KB per us) with the tokens' rows once more
+// per tile at about 2.5 times that from L2, at least 0.3 per unit to issue its
+// products, 1 for each further block per SM, and the sum over a cluster.
+// Measured in a captured run: 64 x 4096 x 11008 takes 14.1 us in clusters of
+// 4 (128 rows) against 19.2 without (32 rows); 64 x 11008 x 4096 takes 12.8
+// without (80 rows) against 14.3 in pairs; 256 x 8192 x 2048 takes 15.5 in
+// pairs against 16.7 without.  Clusters do not pack all SMs (33 of 4 and 15 of
+// 8 fit at one block per SM).
+SplitPlan plan_split(int num_sms, int N, int units, int tokens, int tiles_t, int cols) {
+  SplitPlan best{};
+  double best_us = 1e30;
+  for (int c = 1; c <= 8 && c <= units; c *= 2) {
+    const int sms = std::max(1, num_sms * (c == 1 ? 16 : (c == 2 ? 15 : (c == 4 ? 14 : 13))) / 16);
+    const int64_t cells = int64_t(tiles_t) * c;
+    const int w = i8::cdiv(i8::cdiv(N, i8::BM) * cells, sms);
+    const int64_t tiles = std::max<int64_t>(1, int64_t(w) * sms / cells);
+    const int rows = std::min<int>(i8::BM, std::max<int>(16, i8::cdiv(i8::cdiv(N, tiles), 8) * 8));
+    const int per_block = i8::cdiv(units, c);
+    const double unit_us = std::max(0.3, (rows + 0.4 * tokens) * i8::kUnit / 43600.0);
+    const double us = w * per_block * unit_us + (w - 1) + (c > 1 ? 0.6 + 0.2 * c : 0.0);
+    if (us >= best_us) continue;
+    // two blocks per SM at most: more would have too few stages each
+    const int stage = 2 * (rows + tokens) * i8::BK;
+    // an MMA reads 128 rows from where a tile starts, in the last stage past
+    // its end too
+    const int over = std::max(0, i8::BM * i8::BK + rows * i8::BK - stage);
+    int stages = 0;
+    for (int fit = std::min(w, 512 / cols > 1 ? 2 : 1); fit >= 1 && stages < std::min(3, per_block); --fit)
+      stages = std::min(std::min(per_block, i8::kMaxStages),
+                        (std::min(228 * 1024 / fit - 3072, kSplitSmemMax) - 1024 - over) / stage);
+    const int want = std::max(stages * stage + over, c > 1 ? tokens * i8::BM * 4 : 0) + 1024;
+    // Blocks that share an SM share its 512 columns of tensor memory, and a
+    // block that waits for columns could wait for a cluster whose other blocks
+    // wait for it: so no block takes a smaller part of the SM's 228 KB than of
+    // its columns, and none fits beside a tiled GEMM block (at least 193.25 KB
+    // and all columns).
+    const int share = std::max(int(int64_t(cols) * 228 * 1024 / 512) - 1024, 36 * 1024);
+    best_us = us;
+    best = SplitPlan{c, rows, stages, std::max(want, share)};
+  }
+  return best;
 }
 
 template <typename K>
@@ -522,27 +646,28 @@ staple_status go_tiles(const DeviceInfo& di, const CUtensorMap& a, const CUtenso
   return cudaGetLastError() == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
-template <bool BF16>
+template <bool BF16, int C>
 staple_status go_split(const DeviceInfo& di, const CUtensorMap& w, const CUtensorMap& x,
-                       const i8::Params& p, int tiles_n, int tiles_t, int smem, cudaStream_t st) {
+                       const i8::Params& p, int tiles_t, int smem, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  auto kern = i8::split_kernel<BF16>;
-  if (!opt_in(kern, 226 * 1024, di.device, done)) return STAPLE_ECUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles_n) * unsigned(p.cluster), unsigned(tiles_t));
-  cfg.blockDim = dim3(i8::kThreads);
-  cfg.dynamicSmemBytes = size_t(smem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(p.cluster);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  auto kern = i8::split_kernel<BF16, C>;
+  if (!opt_in(kern, kSplitSmemMax, di.device, done)) return STAPLE_ECUDA;
   cudaError_t ce = cudaSuccess;
-  STP_LAUNCH("matmul_i8_split", st, ce = cudaLaunchKernelEx(&cfg, kern, w, x, p));
+  STP_LAUNCH("matmul_i8_split", st,
+             ce = launch_dependent(kern, dim3(unsigned(i8::cdiv(p.N, p.rows)) * C, unsigned(tiles_t)),
+                                   i8::kThreads, size_t(smem), st, C, w, x, p));
   return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+}
+
+template <bool BF16>
+staple_status go_split_c(const DeviceInfo& di, const CUtensorMap& w, const CUtensorMap& x,
+                         const i8::Params& p, const SplitPlan& pl, int tiles_t, cudaStream_t st) {
+  switch (pl.cluster) {
+    case 1: return go_split<BF16, 1>(di, w, x, p, tiles_t, pl.smem, st);
+    case 2: return go_split<BF16, 2>(di, w, x, p, tiles_t, pl.smem, st);
+    case 4: return go_split<BF16, 4>(di, w, x, p, tiles_t, pl.smem, st);
+    default: return go_split<BF16, 8>(di, w, x, p, tiles_t, pl.smem, st);
+  }
 }
 
 }  // namespace
@@ -583,39 +708,20 @@ staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, in
       return STAPLE_ECUDA;
     return bf16 ? go_tiles<true>(di, ma, mb, mo, p, st) : go_tiles<false>(di, ma, mb, mo, p, st);
   }
-  const int tiles_n = i8::cdiv(N, i8::BM), tiles_t = i8::cdiv(T, i8::kMaxTokens);
+  const int tiles_t = i8::cdiv(T, i8::kMaxTokens);
   p.tokens = std::min(i8::kMaxTokens, i8::cdiv(T, 16) * 16);
   p.cols = 32;
   while (p.cols < p.tokens) p.cols <<= 1;
   p.units = i8::cdiv(K, i8::kUnit);
   p.vec_out = (N % 4) == 0 && (reinterpret_cast<uintptr_t>(y) & uintptr_t(4 * es - 1)) == 0;
-  const int stage_bytes = i8::kWStage + 2 * p.tokens * i8::BK;
-  // The cluster size with the least work on the fullest SM, in k units; a sum
-  // over a cluster costs about as much as four.
-  int best = INT32_MAX, smem = 0;
-  for (int c = 1; c <= i8::kMaxCluster && c <= p.units; ++c) {
-    const int per_sm = i8::cdiv(int64_t(tiles_n) * tiles_t * c, di.num_sms);
-    const int per_block = i8::cdiv(p.units, c);
-    const int cost = per_sm * per_block + (c > 1 ? 4 : 0);
-    if (cost >= best) continue;
-    // as many blocks per SM as there are, if each gets two stages
-    int fit = std::min(per_sm, 512 / p.cols), stages = 0;
-    for (; fit >= 1; --fit) {
-      const int avail = std::min(228 * 1024 / fit - 2048, 225 * 1024) - 1024;
-      stages = std::min(std::min(per_block, i8::kMaxStages), avail / stage_bytes);
-      if (stages >= std::min(2, per_block)) break;
-    }
-    if (fit < 1) continue;
-    best = cost;
-    p.cluster = c;
-    p.stages = stages;
-    smem = split_smem(stages, stage_bytes, p.tokens, p.cols);
-  }
-  if (!tensor_map_2d(&mb, u8, 1, b, K, N, K, i8::BK, i8::BM, sw) ||
+  const SplitPlan pl = plan_split(di.num_sms, N, p.units, p.tokens, tiles_t, p.cols);
+  p.rows = pl.rows;
+  p.stages = pl.stages;
+  if (!tensor_map_2d(&mb, u8, 1, b, K, N, K, i8::BK, uint32_t(p.rows), sw) ||
       !tensor_map_2d(&ma, u8, 1, a, K, T, K, i8::BK, uint32_t(p.tokens), sw))
     return STAPLE_ECUDA;
-  return bf16 ? go_split<true>(di, mb, ma, p, tiles_n, tiles_t, smem, st)
-              : go_split<false>(di, mb, ma, p, tiles_n, tiles_t, smem, st);
+  return bf16 ? go_split_c<true>(di, mb, ma, p, pl, tiles_t, st)
+              : go_split_c<false>(di, mb, ma, p, pl, tiles_t, st);
 }
 
 }  // namespace stp
