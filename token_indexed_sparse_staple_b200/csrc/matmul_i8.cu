@@ -80,7 +80,7 @@ struct Params {
   uint64_t wait_ns;
   // tiles
   int32_t tiles_t, tiles_n, group_t;
-  bool tma_out, vec_scale;
+  bool tma_out;
   // split
   int32_t tokens;        // tokens per tile, rounded up to 16 (the MMA's N)
   int32_t cols;          // tensor-memory columns (a power of two >= 32)
@@ -93,12 +93,13 @@ struct Params {
 
 constexpr int BM = 128, BN = 256, STAGES = 4, kThreads = 192;
 constexpr int A_STAGE = BM * BK, B_STAGE = BN * BK, STAGE_BYTES = A_STAGE + B_STAGE;
-constexpr int kOutBox = 32 * 32 * 4;    // one warp's staged 32 x 32 outputs (fp32 at most)
+// One warp's staged 32 x 32 outputs: two blocks of bf16, or one of fp32.
+constexpr int kOutBox = 32 * 32 * 4;
 // One block per SM, whatever the output type: two would not share the 512
 // columns of tensor memory, and the one that waits for them must not hold
 // shared memory that another kernel could use.
 constexpr int kTilesSmem = 226 * 1024;
-static_assert(1024 + STAGES * STAGE_BYTES + 4 * kOutBox + 256 <= kTilesSmem, "shared memory");
+static_assert(1024 + STAGES * STAGE_BYTES + 4 * kOutBox + 4 * BN * 4 + 256 <= kTilesSmem, "shared memory");
 
 __device__ __forceinline__ void tile_coords(int t, const Params& p, int& mb, int& nb) {
   const int per_group = p.group_t * p.tiles_n;
@@ -107,21 +108,6 @@ __device__ __forceinline__ void tile_coords(int t, const Params& p, int& mb, int
   const int r = t - g * per_group;
   mb = first + r % rows;
   nb = r / rows;
-}
-
-// The 32 channel scales of columns n .. n + 31 (zero past N).
-__device__ __forceinline__ void load_scales(const Params& p, int n, float (&s)[32]) {
-  if (p.vec_scale && n + 32 <= p.N) {
-    const float4* q = reinterpret_cast<const float4*>(p.b_scale + n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 v = __ldg(q + i);
-      s[4 * i] = v.x; s[4 * i + 1] = v.y; s[4 * i + 2] = v.z; s[4 * i + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[i] = n + i < p.N ? __ldg(p.b_scale + n + i) : 0.0f;
-  }
 }
 
 template <bool BF16>
@@ -133,7 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * A_STAGE;
   uint8_t* s_out = sB + STAGES * B_STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_out + 4 * kOutBox);
+  float* s_scale = reinterpret_cast<float*>(s_out + 4 * kOutBox);   // [4 warps][256]
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + 4 * BN);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
@@ -228,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_drain(dbar, 0);
   } else {
     const int q = warp & 3;
-    uint8_t* stg = s_out + q * kOutBox;
+    uint8_t* box = s_out + q * kOutBox;
+    float* scales = s_scale + q * BN;      // the tile's channel scales, a copy per warp
     int iter = 0;
     for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++iter) {
       const int buf = iter & 1;
@@ -236,6 +224,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_coords(t, p, mb, nb);
       const int m0 = mb * BM + q * 32, m = m0 + lane;
       const float sa = m < p.T ? __ldg(p.a_scale + m) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < BN / 32; ++i) {
+        const int n = nb * BN + i * 32 + lane;
+        scales[i * 32 + lane] = n < p.N ? __ldg(p.b_scale + n) : 0.0f;
+      }
+      __syncwarp();
       const bool ok = mbar_wait(&tfull[buf], uint32_t(iter >> 1) & 1, abort_flag, p.err, p.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
@@ -244,18 +238,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < BN / 32; ++c) {
         const int n = nb * BN + c * 32;
         if (n >= p.N) break;          // the same for the whole warp
-        float sb[32];
-        load_scales(p, n, sb);
+        uint8_t* stg = box + (BF16 ? (c & 1) * (kOutBox / 2) : 0);
         uint32_t r[32];
         tmem_ld32(tacc + c * 32, r);
         tmem_ld_wait(r);
         float v[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = float(int(r[i])) * sa * sb[i];
+        for (int i = 0; i < 8; ++i) {
+          const float4 sb = *reinterpret_cast<const float4*>(scales + c * 32 + 4 * i);
+          v[4 * i] = float(int(r[4 * i])) * sa * sb.x;
+          v[4 * i + 1] = float(int(r[4 * i + 1])) * sa * sb.y;
+          v[4 * i + 2] = float(int(r[4 * i + 2])) * sa * sb.z;
+          v[4 * i + 3] = float(int(r[4 * i + 3])) * sa * sb.w;
+        }
         // stage the 32 x 32 block, swizzled as the TMA store expects it (and
         // free of bank conflicts either way)
-        if (p.tma_out) {
-          if (lane == 0) bulk_wait_read0();
+        if (p.tma_out && lane == 0) {
+          // (bf16: the block before this one may still be on its way out)
+          if constexpr (BF16) bulk_wait_read1();
+          else bulk_wait_read0();
         }
         __syncwarp();
         if constexpr (BF16) {
@@ -695,7 +696,6 @@ staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, in
   p.tiles_n = i8::cdiv(N, i8::BN);
   if (T > i8::kMaxTokens && int64_t(p.tiles_t) * p.tiles_n >= di.num_sms) {
     p.group_t = 16;
-    p.vec_scale = (reinterpret_cast<uintptr_t>(b_scale) & 15u) == 0;
     p.tma_out = (int64_t(N) * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
     if (!tensor_map_2d(&ma, u8, 1, a, K, T, K, i8::BK, i8::BM, sw) ||
         !tensor_map_2d(&mb, u8, 1, b, K, N, K, i8::BK, i8::BN, sw))
