@@ -523,6 +523,30 @@ staple_status staple_matmul_i8(staple_context* ctx, staple_dtype dtype, int32_t 
                                int32_t K, const int8_t* a, const float* a_scale, const int8_t* b,
                                const float* b_scale, void* y, staple_stream stream);
 
+/* The layer's forward pass with weights in 8 bits, for serving (no g, h or z
+ * is kept for a backward pass); any T.  x is quantised by rows, g and u are
+ * 8-bit products rounded to bf16, z = SiLU(g) * (u + E[id]) is rounded to bf16
+ * and quantised by rows, y is an 8-bit product.  Four launches:
+ * staple_quant_rows and staple_matmul_i8 twice each, the second quantisation
+ * with the gating in front of it.
+ *   x, y           bf16 [T][D];  y may be x
+ *   embed          as for staple_ffn_fwd (bf16 rows), STAPLE_EMBED_REPLACE_UP
+ *                  included
+ *   w_gate_up      int8 [2F][D]: W_gate's rows, then W_up's (REPLACE_UP: the
+ *                  first F rows are all that is read), and gate_up_scale fp32
+ *                  [2F], one per row, as staple_quant_rows makes them
+ *   w_down         int8 [D][F] with down_scale fp32 [D]
+ *   workspace      staple_ffn_i8_workspace_bytes(T, D, F), 256-byte aligned;
+ *                  no initial contents; one call at a time per workspace
+ * bf16 and int8 tensors 16-byte aligned; D and F multiples of 16, at most
+ * 32768. */
+staple_status staple_ffn_fwd_i8(staple_context* ctx, int32_t T, int32_t D, int32_t F,
+                                const void* x, const staple_embed* embed, const int8_t* w_gate_up,
+                                const float* gate_up_scale, const int8_t* w_down,
+                                const float* down_scale, void* y, void* workspace,
+                                size_t workspace_bytes, staple_stream stream);
+size_t staple_ffn_i8_workspace_bytes(int32_t T, int32_t D, int32_t F);
+
 /* ------------------------------------------------ host optimizer (AdamW) */
 
 typedef struct staple_adamw {

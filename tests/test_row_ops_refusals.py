@@ -122,3 +122,26 @@ def test_matmul_i8(lib, ctx):
         (dict(y=None), E), (dict(a=OK_PTR + 8), E), (dict(b=ODD), E), (dict(a_scale=OK_PTR + 2), E),
         (dict(b_scale=ODD), E), (dict(y=OK_PTR + 2), E), (dict(T=0), stp.STAPLE_OK),
     ])
+
+
+def test_ffn_fwd_i8(lib, ctx):
+    ws = stp.staple_ffn_i8_workspace_bytes(5, 32, 48)
+    assert ws >= 5 * (32 + 2 * 48 * 2 + 48 + 8) and ws % 256 == 0
+    w = stp.staple_ffn_i8_workspace_bytes
+    assert w(-1, 32, 48) == 0 and w(5, 8, 48) == 0 and w(5, 32, 40) == 0 and w(5, 32784, 48) == 0
+    e = stp.make_embed(stp.STAPLE_EMBED_TABLE, OK_PTR, 48, OK_PTR, 10)
+    good = dict(ctx=ctx, T=5, D=32, F=48, x=OK_PTR, embed=C.byref(e), w_gate_up=OK_PTR, gus=OK_PTR,
+                w_down=OK_PTR, ds=OK_PTR + 4, y=OK_PTR, workspace=OK_PTR, wsb=ws, stream=None)
+    bad_pitch = stp.make_embed(stp.STAPLE_EMBED_TABLE, OK_PTR, 40, OK_PTR, 10)
+    bad_base = stp.make_embed(stp.STAPLE_EMBED_TABLE, OK_PTR + 2, 48, OK_PTR, 10)
+    stem_none = stp.make_embed(stp.STAPLE_EMBED_NONE, flags=stp.STAPLE_EMBED_REPLACE_UP)
+    check(lib.staple_ffn_fwd_i8, good, [
+        (dict(ctx=None), E), (dict(T=-1), E), (dict(D=24), E), (dict(F=40), E), (dict(F=0), E),
+        (dict(D=32784), U), (dict(F=32784), U), (dict(x=None), E), (dict(x=OK_PTR + 8), E),
+        (dict(y=None), E), (dict(w_gate_up=None), E), (dict(w_down=OK_PTR + 4), E),
+        (dict(gus=None), E), (dict(ds=ODD), E), (dict(workspace=None), E),
+        (dict(workspace=OK_PTR + 16), E), (dict(wsb=ws - 1), E), (dict(embed=C.byref(bad_pitch)), E),
+        (dict(embed=C.byref(bad_base)), E), (dict(embed=C.byref(stem_none)), E),
+        (dict(T=0), stp.STAPLE_OK),
+    ])
+    assert lib.staple_ffn_fwd_i8(*dict(good, embed=None).values()) == stp.STAPLE_ECUDA

@@ -331,3 +331,16 @@ def staple_matmul_i8(ctx, dtype, T, N, K, a, a_scale, b, b_scale, y, stream=None
     """y = (a b^T) a_scale b_scale with 8-bit a [T][K] and b [N][K] (see include/staple.h)."""
     _ok(lib().staple_matmul_i8(ctx, dtype, T, N, K, _p(a), _p(a_scale), _p(b), _p(b_scale), _p(y),
                                _stream(stream)), "staple_matmul_i8")
+
+
+def staple_ffn_i8_workspace_bytes(T: int, D: int, F: int) -> int:
+    return int(lib().staple_ffn_i8_workspace_bytes(T, D, F))
+
+
+def staple_ffn_fwd_i8(ctx, T, D, F, x, embed, w_gate_up, gate_up_scale, w_down, down_scale, y,
+                      workspace, workspace_bytes, stream=None):
+    """The layer with 8-bit weights (see include/staple.h)."""
+    e = C.byref(embed) if embed is not None else None
+    _ok(lib().staple_ffn_fwd_i8(ctx, T, D, F, _p(x), e, _p(w_gate_up), _p(gate_up_scale),
+                                _p(w_down), _p(down_scale), _p(y), _p(workspace), workspace_bytes,
+                                _stream(stream)), "staple_ffn_fwd_i8")

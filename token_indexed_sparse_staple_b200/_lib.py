@@ -82,6 +82,9 @@ SIGNATURES = {
                                    P(staple_drop), vp, vp, vp, vp, vp, sz, vp]),
     "staple_dropout": (c_status, [vp, C.c_int, i32, i32, vp, vp, P(staple_drop), vp, vp]),
     "staple_matmul_i8": (c_status, [vp, C.c_int, i32, i32, i32, vp, vp, vp, vp, vp, vp]),
+    "staple_ffn_fwd_i8": (c_status, [vp, i32, i32, i32, vp, P(staple_embed), vp, vp, vp, vp, vp, vp,
+                                     sz, vp]),
+    "staple_ffn_i8_workspace_bytes": (sz, [i32, i32, i32]),
     "staple_quant_rows": (c_status, [vp, C.c_int, i32, i32, vp, vp, vp, vp]),
 }
 

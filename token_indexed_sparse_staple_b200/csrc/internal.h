@@ -158,6 +158,12 @@ constexpr int kQuantMaxD = 32768;
 staple_status launch_quant_rows(const DeviceInfo& di, bool bf16, int T, int D, const void* x, int8_t* q, float* scale,
                                 cudaStream_t st);
 
+// z = SiLU(g) (u + E) of an 8-bit layer, straight to 8 bits: gu is [T][2F]
+// (g, then u) or, without u, [T][F]
+staple_status launch_gate_quant(const DeviceInfo& di, int T, int F, const void* gu, bool up,
+                                const staple_embed* e, int8_t* q, float* scale, int32_t* err,
+                                cudaStream_t st);
+
 // matmul_i8.cu: K is at most kI8MaxK, so that no sum of products of two 8-bit
 // numbers leaves 32 bits (2^14 K < 2^31)
 constexpr int kI8MaxK = (1 << 17) - 16;

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int ntiles = p.tiles_t * p.tiles_n, kblocks = (p.K + BK - 1) / BK;
+  wait_prior_kernels();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -642,9 +643,11 @@ staple_status go_tiles(const DeviceInfo& di, const CUtensorMap& a, const CUtenso
   const int ntiles = p.tiles_t * p.tiles_n;
   const int avail = std::max(1, di.num_sms - di.sm_reserve);
   const int per = i8::cdiv(ntiles, avail);
+  cudaError_t ce = cudaSuccess;
   STP_LAUNCH("matmul_i8", st,
-             kern<<<i8::cdiv(ntiles, per), i8::kThreads, i8::kTilesSmem, st>>>(a, b, o, p));
-  return cudaGetLastError() == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+             ce = launch_dependent(kern, dim3(unsigned(i8::cdiv(ntiles, per))), i8::kThreads,
+                                   i8::kTilesSmem, st, 1, a, b, o, p));
+  return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
 template <bool BF16, int C>

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
   const bool row_ok = row < p.T;
   const int G = (p.D + kGroup - 1) / kGroup;
   const int64_t base = row * p.D;
+  wait_prior_kernels();
   Raw8<BF16> xr[NV], rr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) aw[i][j] = ab[i][j] = 0.0f;
+  wait_prior_kernels();
   DropKey key{};
   if (DROP) key = drop_key(p.drop);
   int buf = 0;
@@ -357,6 +359,7 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
     fence_barrier_init();
   }
   __syncthreads();
+  wait_prior_kernels();
   const int64_t row0 = int64_t(blockIdx.x) * rpb + rg, step = int64_t(gridDim.x) * rpb;
   auto fill = [&](int64_t row, int s) {
     uint8_t* dst = ring + s * stage_bytes;
@@ -555,7 +558,7 @@ constexpr int kWgCols = 32, kWgSlices = 8;
 __global__ void __launch_bounds__(kWgCols* kWgSlices)
     norm_wgrad_kernel(const float* part, int blocks, int D, float* dw, float* db) {
   __shared__ float s[kWgSlices][kWgCols];
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial sums are written
+  wait_prior_kernels();   // the partial sums are written
   const int cx = threadIdx.x % kWgCols, sl = threadIdx.x / kWgCols;
   const int d = blockIdx.x * kWgCols + cx;
   float* dst = blockIdx.y ? db : dw;
@@ -596,11 +599,12 @@ bool vec_ok(int D, std::initializer_list<const void*> ps) {
 
 template <bool BF16, int NV, bool VEC>
 staple_status fwd_go(const FwdParams& p, int grid, int block, cudaStream_t st) {
-  if (p.drop.rng)
-    STP_LAUNCH("norm_fwd", st, norm_fwd_kernel<BF16, NV, VEC, true><<<grid, block, 0, st>>>(p));
-  else
-    STP_LAUNCH("norm_fwd", st, norm_fwd_kernel<BF16, NV, VEC, false><<<grid, block, 0, st>>>(p));
-  return cudaGetLastError() == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+  cudaError_t ce = cudaSuccess;
+  STP_LAUNCH("norm_fwd", st,
+             ce = launch_dependent(p.drop.rng ? norm_fwd_kernel<BF16, NV, VEC, true>
+                                              : norm_fwd_kernel<BF16, NV, VEC, false>,
+                                   dim3(unsigned(grid)), unsigned(block), 0, st, 1, p));
+  return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
 template <bool BF16, bool VEC>
@@ -616,10 +620,11 @@ constexpr int rows_in_flight(bool bf16, int nv) { return nv == 1 ? (bf16 ? 4 : 2
 
 template <bool BF16, int NV, bool VEC, bool DROP>
 staple_status bwd_go(const BwdParams& p, int grid, int block, size_t smem, cudaStream_t st) {
+  cudaError_t ce = cudaSuccess;
   STP_LAUNCH("norm_bwd", st,
-             norm_bwd_kernel<BF16, NV, rows_in_flight(BF16, NV), VEC, DROP>
-             <<<grid, block, smem, st>>>(p));
-  return cudaGetLastError() == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+             ce = launch_dependent(norm_bwd_kernel<BF16, NV, rows_in_flight(BF16, NV), VEC, DROP>,
+                                   dim3(unsigned(grid)), unsigned(block), smem, st, 1, p));
+  return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
 template <bool BF16, bool VEC, bool DROP>
@@ -674,8 +679,10 @@ staple_status ring_go(const DeviceInfo& di, const RingParams& p, int grid, int b
       return STAPLE_ECUDA;
     attr_done.fetch_or(bit);
   }
-  STP_LAUNCH("norm_bwd", st, kern<<<grid, block, smem, st>>>(p));
-  return cudaGetLastError() == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+  cudaError_t ce = cudaSuccess;
+  STP_LAUNCH("norm_bwd", st,
+             ce = launch_dependent(kern, dim3(unsigned(grid)), unsigned(block), smem, st, 1, p));
+  return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
 template <bool BF16, bool DROP>
@@ -713,6 +720,7 @@ struct DropoutParams {
 
 template <bool BF16, bool VEC, bool DROP>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams p) {
+  wait_prior_kernels();
   const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (u >= p.units) return;
   int64_t off = u * kGroup;
@@ -739,11 +747,12 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams p) {
 template <bool BF16, bool VEC>
 staple_status dropout_go(const DropoutParams& p, cudaStream_t st) {
   const unsigned grid = unsigned((p.units + 255) / 256);
-  if (p.drop.rng)
-    STP_LAUNCH("dropout", st, dropout_kernel<BF16, VEC, true><<<grid, 256, 0, st>>>(p));
-  else
-    STP_LAUNCH("dropout", st, dropout_kernel<BF16, VEC, false><<<grid, 256, 0, st>>>(p));
-  return cudaGetLastError() == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+  cudaError_t ce = cudaSuccess;
+  STP_LAUNCH("dropout", st,
+             ce = launch_dependent(p.drop.rng ? dropout_kernel<BF16, VEC, true>
+                                              : dropout_kernel<BF16, VEC, false>,
+                                   dim3(grid), 256, 0, st, 1, p));
+  return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
 }  // namespace
@@ -818,19 +827,10 @@ staple_status launch_norm_bwd(const DeviceInfo& di, bool bf16, bool rms, int T, 
                             : bwd_nv<false, false, false>(p, nv, grid, block, smem, st));
   }
   if (r != STAPLE_OK || !p.part) return r;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cdiv(D, kWgCols), 2);
-  cfg.blockDim = dim3(kWgCols * kWgSlices);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   cudaError_t ce = cudaSuccess;
-  const float* cpart = part;
   STP_LAUNCH("norm_wgrad", st,
-             ce = cudaLaunchKernelEx(&cfg, norm_wgrad_kernel, cpart, grid, D, dw, db));
+             ce = launch_dependent(norm_wgrad_kernel, dim3(unsigned(cdiv(D, kWgCols)), 2),
+                                   kWgCols * kWgSlices, 0, st, 1, part, grid, D, dw, db));
   return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 

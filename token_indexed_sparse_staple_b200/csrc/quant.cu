@@ -29,6 +29,13 @@ struct QuantParams {
   int8_t* q;
   float* scale;
   int32_t T, D, tpr;
+  // GATE: x holds g [T][pitch] and, `up` elements further on, u (0: none)
+  int64_t pitch;
+  int32_t up;
+  const uint16_t* e_base;    // E rows; NULL: none
+  int64_t e_pitch, e_rows;
+  const int32_t* e_index;
+  int32_t* err;
 };
 
 constexpr float kRintMagic = 12582912.0f;   // 1.5 * 2^23
@@ -42,7 +49,9 @@ __device__ __forceinline__ uint32_t q_exact(float x, double scale) {
   return uint32_t(int(d)) & 0xffu;
 }
 
-template <bool BF16, int NV, bool VEC>
+// GATE: the row is not x but the layer's gated product z = SiLU(g) (u + E),
+// rounded to bf16 as the layer stores it, which thus never goes to memory.
+template <bool BF16, int NV, bool VEC, bool GATE>
 // (bf16: 64 registers, so that 32 warps share an SM)
 __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const QuantParams p) {
   __shared__ uint32_t red[32];
@@ -52,13 +61,34 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
   const bool row_ok = row < p.T;
   const int G = (p.D + kGroup - 1) / kGroup;
   const int64_t base = row * p.D;
+  wait_prior_kernels();
+  const uint16_t* e_row = nullptr;
+  if (GATE && row_ok && p.e_base) {
+    const int64_t idx = p.e_index[row];
+    if (idx < 0 || idx >= p.e_rows) report(p.err, STAPLE_EIDRANGE);
+    else e_row = p.e_base + idx * p.e_pitch;
+  }
   Raw8<BF16> xr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int g = t + i * p.tpr;
     xr[i] = zero_raw8<BF16>();
-    if (row_ok && g < G)
-      xr[i] = load_raw8<BF16, VEC>(p.x, base + g * kGroup, min(kGroup, p.D - g * kGroup));
+    if (row_ok && g < G) {
+      if constexpr (GATE) {
+        const int64_t off = row * p.pitch + g * kGroup;
+        const Raw8<true> gr = load_raw8<true, true>(p.x, off, kGroup);
+        Raw8<true> ur = zero_raw8<true>(), er = zero_raw8<true>();
+        if (p.up) ur = load_raw8<true, true>(p.x, off + p.up, kGroup);
+        if (e_row) er = load_raw8<true, true>(e_row, g * kGroup, kGroup);
+        float z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          z[j] = gr.get(j) * sigmoid_f(gr.get(j)) * (ur.get(j) + er.get(j));
+        xr[i] = pack_raw8<true>(z);
+      } else {
+        xr[i] = load_raw8<BF16, VEC>(p.x, base + g * kGroup, min(kGroup, p.D - g * kGroup));
+      }
+    }
   }
   // the largest |x| as bits: a NaN is above the infinity, which is above
   // every finite number
@@ -143,41 +173,70 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
   }
 }
 
-template <bool BF16, bool VEC>
-void go(const QuantParams& p, int nv, unsigned grid, int block, cudaStream_t st) {
+template <bool BF16, bool VEC, bool GATE>
+cudaError_t go(const DeviceInfo& di, QuantParams p, cudaStream_t st) {
+  // few rows: as many threads per row as there are groups; many: up to eight
+  // groups per thread, whose loads are in flight together and whose maximum
+  // is found with few instructions per element (16384 x 8192 bf16: 125 us with
+  // two, 80 with four, 73 with eight)
+  const int G = groups_of(p.D);
+  const int few = G > 2048 ? 8 : (G > 1024 ? 4 : (G > 512 ? 2 : 1));
+  const int many = G > 128 ? 8 : (G > 64 ? 4 : (G > 32 ? 2 : 1));
+  const int nv = p.T <= 2 * di.num_sms ? few : many;
+  p.tpr = threads_per_row(G, nv);
+  const int rpb = std::max(1, 128 / p.tpr);
+  const dim3 grid(unsigned((int64_t(p.T) + rpb - 1) / rpb));
+  const unsigned block = unsigned(rpb * p.tpr);
   switch (nv) {
-    case 1: quant_rows_kernel<BF16, 1, VEC><<<grid, block, 0, st>>>(p); break;
-    case 2: quant_rows_kernel<BF16, 2, VEC><<<grid, block, 0, st>>>(p); break;
-    case 4: quant_rows_kernel<BF16, 4, VEC><<<grid, block, 0, st>>>(p); break;
-    default: quant_rows_kernel<BF16, 8, VEC><<<grid, block, 0, st>>>(p); break;
+    case 1: return launch_dependent(quant_rows_kernel<BF16, 1, VEC, GATE>, grid, block, 0, st, 1, p);
+    case 2: return launch_dependent(quant_rows_kernel<BF16, 2, VEC, GATE>, grid, block, 0, st, 1, p);
+    case 4: return launch_dependent(quant_rows_kernel<BF16, 4, VEC, GATE>, grid, block, 0, st, 1, p);
+    default: return launch_dependent(quant_rows_kernel<BF16, 8, VEC, GATE>, grid, block, 0, st, 1, p);
   }
 }
 
 }  // namespace
 
-staple_status launch_quant_rows(const DeviceInfo& di, bool bf16, int T, int D, const void* x, int8_t* q, float* scale,
-                                cudaStream_t st) {
+staple_status launch_quant_rows(const DeviceInfo& di, bool bf16, int T, int D, const void* x,
+                                int8_t* q, float* scale, cudaStream_t st) {
   if (T == 0) return STAPLE_OK;
-  QuantParams p{x, q, scale, T, D, 0};
-  const int G = groups_of(D);
-  // few rows: as many threads per row as there are groups; many: up to eight
-  // groups per thread, whose loads are in flight together and whose maximum
-  // is found with few instructions per element
-  const int few = G > 2048 ? 8 : (G > 1024 ? 4 : (G > 512 ? 2 : 1));
-  const int many = G > 128 ? 8 : (G > 64 ? 4 : (G > 32 ? 2 : 1));
-  const int nv = T <= 2 * di.num_sms ? few : many;
-  p.tpr = threads_per_row(G, nv);
-  const int rpb = std::max(1, 128 / p.tpr);
-  const unsigned grid = unsigned((int64_t(T) + rpb - 1) / rpb);
-  const int block = rpb * p.tpr;
+  QuantParams p{};
+  p.x = x;
+  p.q = q;
+  p.scale = scale;
+  p.T = T;
+  p.D = D;
   const bool vec = D % kGroup == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 &&
                    (reinterpret_cast<uintptr_t>(q) & 7u) == 0;
+  cudaError_t ce = cudaSuccess;
   STP_LAUNCH("quant_rows", st,
-             if (bf16) { if (vec) go<true, true>(p, nv, grid, block, st);
-                         else go<true, false>(p, nv, grid, block, st); }
-             else { if (vec) go<false, true>(p, nv, grid, block, st);
-                    else go<false, false>(p, nv, grid, block, st); });
-  return cudaGetLastError() == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+             ce = bf16 ? (vec ? go<true, true, false>(di, p, st) : go<true, false, false>(di, p, st))
+                       : (vec ? go<false, true, false>(di, p, st) : go<false, false, false>(di, p, st)));
+  return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+}
+
+staple_status launch_gate_quant(const DeviceInfo& di, int T, int F, const void* gu, bool up,
+                                const staple_embed* e, int8_t* q, float* scale, int32_t* err,
+                                cudaStream_t st) {
+  if (T == 0) return STAPLE_OK;
+  QuantParams p{};
+  p.x = gu;
+  p.q = q;
+  p.scale = scale;
+  p.T = T;
+  p.D = F;
+  p.pitch = up ? 2 * int64_t(F) : F;
+  p.up = up ? F : 0;
+  if (e && e->mode != STAPLE_EMBED_NONE) {
+    p.e_base = static_cast<const uint16_t*>(e->base);
+    p.e_pitch = e->row_pitch;
+    p.e_rows = e->n_rows;
+    p.e_index = e->index;
+  }
+  p.err = err;
+  cudaError_t ce = cudaSuccess;
+  STP_LAUNCH("gate_quant", st, ce = (go<true, true, true>(di, p, st)));
+  return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
 }  // namespace stp

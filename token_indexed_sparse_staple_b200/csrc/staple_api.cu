@@ -838,4 +838,69 @@ staple_status staple_matmul_i8(staple_context* ctx, staple_dtype dtype, int32_t 
                                ctx->d_err, cs(stream));
 }
 
+namespace {
+
+// An 8-bit layer's scratch: x and z in 8 bits with their scales, and g, u.
+struct I8Layout {
+  size_t xq, xs, gu, zq, zs, bytes;
+};
+I8Layout i8_layout(int32_t T, int32_t D, int32_t F) {
+  I8Layout l{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t p = at;
+    at += (n + 255) & ~size_t(255);
+    return p;
+  };
+  l.xq = take(size_t(T) * D);
+  l.xs = take(size_t(T) * 4);
+  l.gu = take(size_t(T) * 2 * F * 2);
+  l.zq = take(size_t(T) * F);
+  l.zs = take(size_t(T) * 4);
+  l.bytes = at;
+  return l;
+}
+
+staple_status check_i8_dims(int32_t T, int32_t D, int32_t F) {
+  if (T < 0 || D <= 0 || F <= 0 || D % 16 || F % 16) return STAPLE_EINVAL;
+  return D > stp::kQuantMaxD || F > stp::kQuantMaxD ? STAPLE_EUNSUPPORTED : STAPLE_OK;
+}
+
+}  // namespace
+
+size_t staple_ffn_i8_workspace_bytes(int32_t T, int32_t D, int32_t F) {
+  return check_i8_dims(T, D, F) == STAPLE_OK ? i8_layout(T, D, F).bytes : 0;
+}
+
+staple_status staple_ffn_fwd_i8(staple_context* ctx, int32_t T, int32_t D, int32_t F,
+                                const void* x, const staple_embed* embed, const int8_t* w_gate_up,
+                                const float* gate_up_scale, const int8_t* w_down,
+                                const float* down_scale, void* y, void* workspace,
+                                size_t workspace_bytes, staple_stream stream) {
+  if (!ctx) return STAPLE_EINVAL;
+  STP_TRY(check_i8_dims(T, D, F));
+  STP_TRY(check_embed(embed, STAPLE_BF16, F));
+  if (T == 0) return STAPLE_OK;
+  if (!ptrs_ok(STAPLE_BF16, {x, w_gate_up, w_down, y})) return STAPLE_EINVAL;
+  if (!gate_up_scale || !down_scale || !aligned_to(gate_up_scale, 4) || !aligned_to(down_scale, 4))
+    return STAPLE_EINVAL;
+  const I8Layout l = i8_layout(T, D, F);
+  if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < l.bytes) return STAPLE_EINVAL;
+  STP_TRY(set_device(ctx));
+  stp::TraceScope trace_scope(ctx->tracer);
+  cudaStream_t st = cs(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int8_t* xq = reinterpret_cast<int8_t*>(ws + l.xq);
+  int8_t* zq = reinterpret_cast<int8_t*>(ws + l.zq);
+  float* xs = reinterpret_cast<float*>(ws + l.xs);
+  float* zs = reinterpret_cast<float*>(ws + l.zs);
+  const bool up = !replaces_up(embed);
+  STP_TRY(stp::launch_quant_rows(ctx->di, true, T, D, x, xq, xs, st));
+  STP_TRY(stp::launch_matmul_i8(ctx->di, true, T, up ? 2 * F : F, D, xq, xs, w_gate_up,
+                                gate_up_scale, ws + l.gu, ctx->d_err, st));
+  STP_TRY(stp::launch_gate_quant(ctx->di, T, F, ws + l.gu, up, embed, zq, zs, ctx->d_err, st));
+  return stp::launch_matmul_i8(ctx->di, true, T, D, F, zq, zs, w_down, down_scale, y, ctx->d_err,
+                               st);
+}
+
 }  // extern "C"

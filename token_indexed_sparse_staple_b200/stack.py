@@ -25,6 +25,15 @@ the computation runs in the library's kernels).
   multi-stream CUDA graph and replayed (Decode row: grouped lookups and the
   model in one multi-stream CUDA graph).
 
+- With `norms`, a stack is the residual stream of a pre-norm transformer's
+  FFN sublayers instead of the bare chain:
+      x_{l+1} = x_l + dropout(FFN_l(norm_l(x_l)))
+  Each residual add, its dropout and the next layer's norm are one kernel, and
+  so are the backward pass of a norm, the residual's gradient and the dropout
+  in front of it.  No dropout mask is stored: the backward pass draws it again
+  from the step's {seed, offset} and the layer's site.
+- Decode layers may have their weights in 8 bits (LayerWeightsI8).
+
 torch supplies device memory, pinned host memory, streams and events.
 """
 from __future__ import annotations
@@ -39,6 +48,38 @@ class LayerWeights:
     w_gate: object   # [F][D] bf16
     w_up: object     # [F][D] bf16
     w_down: object   # [D][F] bf16
+
+
+@dataclass
+class LayerWeightsI8:
+    """A decode layer's weights in 8 bits, one scale per row."""
+    w_gate_up: object      # [2F][D] int8: W_gate's rows, then W_up's
+    gate_up_scale: object  # [2F] fp32
+    w_down: object         # [D][F] int8
+    down_scale: object     # [D] fp32
+
+
+def quantise_layer(ctx, w: LayerWeights, stream=None) -> LayerWeightsI8:
+    """The 8-bit copy of a layer's bf16 weights, made on `stream` (default:
+    torch's current stream)."""
+    import torch
+    F, D = w.w_gate.shape
+    gu = torch.empty((2 * F, D), dtype=torch.int8, device="cuda")
+    gus = torch.empty(2 * F, dtype=torch.float32, device="cuda")
+    down = torch.empty((D, F), dtype=torch.int8, device="cuda")
+    ds = torch.empty(D, dtype=torch.float32, device="cuda")
+    for src, q, s in ((w.w_gate, gu[:F], gus[:F]), (w.w_up, gu[F:], gus[F:]), (w.w_down, down, ds)):
+        stp.staple_quant_rows(ctx, stp.STAPLE_BF16, *src.shape, src, q, s, stream=stream)
+    return LayerWeightsI8(gu, gus, down, ds)
+
+
+@dataclass
+class NormWeights:
+    """The norm in front of a layer."""
+    weight: object = None            # [D] bf16, or None (ones)
+    bias: object = None              # [D] bf16, or None (zeros)
+    kind: int = stp.STAPLE_NORM_RMS
+    eps: float = 1e-5
 
 
 class GroupedTables:
@@ -147,11 +188,19 @@ class TrainStack:
     every layer returned to host memory."""
 
     def __init__(self, ctx, weights: list, tables: GroupedTables, T: int, D: int, F: int, V: int,
-                 freeze_up: bool = False, keep_dy: bool = False, de_return: str = "dma"):
+                 freeze_up: bool = False, keep_dy: bool = False, de_return: str = "dma",
+                 norms=None, dropout: float = 0.0, rng=None):
         """keep_dy keeps every layer's incoming gradient (L buffers instead of
-        two alternating ones), so each layer can be checked on its own inputs.
+        two alternating ones), so each layer can be checked on its own inputs
+        (with norms the residual stream's gradients too, in dstream).
         de_return: "dma" (copy engine, U known on the host) or "kernel"
-        (staple_embed_grad_to_host, U read on the device)."""
+        (staple_embed_grad_to_host, U read on the device).
+        norms: one NormWeights per layer, which makes the stack the residual
+        stream described above; dropout is then the probability of the
+        dropouts in front of the residual adds, drawn from rng, a device int64
+        tensor {seed, offset} that the caller advances by L after each step
+        (site l is layer l's).  The gradients of x_0 and of the norms are in
+        dx0 and dnorm[l] = (dw, db) after a step."""
         assert de_return in ("dma", "kernel")
         self.de_return = de_return
         import torch
@@ -179,6 +228,23 @@ class TrainStack:
             host_unique=[torch.empty(T, dtype=torch.int32).pin_memory() for _ in range(L)],
             host_U=[torch.zeros(1, dtype=torch.int32).pin_memory() for _ in range(L)],
             ws=torch.zeros(max(wsb, 256), dtype=torch.uint8, device="cuda"), wsb=wsb)
+        self.norms = list(norms) if norms is not None else None
+        if self.norms is not None:
+            assert len(self.norms) == L
+            assert dropout == 0.0 or rng is not None
+            self.rng = rng
+            self.drops = [stp.make_drop(dropout, rng, l) for l in range(L)]
+            self.n = [torch.empty((T, D), **bf) for _ in range(L)]      # the layers' inputs
+            self.y = torch.empty((T, D), **bf)                          # a layer's output
+            self.mean, self.rstd = ([torch.empty(T, **f32) for _ in range(L)] for _ in range(2))
+            self.dnorm = [(torch.empty(D, **f32), torch.empty(D, **f32)) for _ in range(L)]
+            self.dn = torch.empty((T, D), **bf)                         # gradient of norm_l's output
+            self.dstream = [torch.empty((T, D), **bf) for _ in range(L if keep_dy else 2)]
+            self.dx0 = None
+            self.nws = torch.empty(max(stp.staple_norm_workspace_bytes(T, D), 16),
+                                   dtype=torch.uint8, device="cuda")
+        else:
+            assert dropout == 0.0
         self.retr = [Retrieval(T, F, self.G, tables.n_groups) for _ in range(2)]
         self.pf, self.pf_side, self.copy = (torch.cuda.Stream() for _ in range(3))
         self.host_ready = torch.cuda.Event()   # the last step's dE rows are in host memory
@@ -191,6 +257,12 @@ class TrainStack:
         self.pf.wait_event(r.free)
         issue_dedup(self.ctx, r, ids, self.V, self.pf)
         issue_group(self.ctx, r, self.tables, 0, self.pf, self.pf_side)
+
+    def _norm_fwd(self, l: int, x, st, **kw):
+        nw = self.norms[l]
+        stp.staple_norm_fwd(self.ctx, stp.STAPLE_BF16, nw.kind, self.T, self.D, x, self.n[l],
+                            weight=nw.weight, bias=nw.bias, eps=nw.eps, mean=self.mean[l],
+                            rstd=self.rstd[l], stream=st, **kw)
 
     def step(self, ids, x0, dy_top, next_ids=None, stream=None):
         """One training step on `stream` (default: torch's current stream).
@@ -216,14 +288,25 @@ class TrainStack:
             with torch.cuda.stream(st):
                 b.xs[0].copy_(x0)
         # forward
+        if self.norms is not None:
+            self._norm_fwd(0, b.xs[0], st)
         for l in range(self.L):
             gi = l // self.G
             if l % self.G == 0:
                 st.wait_event(r.ready[gi])
             w = self.W[l]
-            stp.staple_ffn_fwd(self.ctx, stp.STAPLE_BF16, T, D, F, b.xs[l], r.embed(l), w.w_gate,
-                               w.w_up, w.w_down, b.z[l], b.xs[l + 1], b.g[l], b.h[l], b.ws, b.wsb,
+            x, y = (b.xs[l], b.xs[l + 1]) if self.norms is None else (self.n[l], self.y)
+            stp.staple_ffn_fwd(self.ctx, stp.STAPLE_BF16, T, D, F, x, r.embed(l), w.w_gate,
+                               w.w_up, w.w_down, b.z[l], y, b.g[l], b.h[l], b.ws, b.wsb,
                                stream=st)
+            if self.norms is None:
+                continue
+            if l + 1 < self.L:     # the residual add and the next layer's norm
+                self._norm_fwd(l + 1, self.y, st, residual=b.xs[l], drop=self.drops[l],
+                               sum=b.xs[l + 1])
+            else:
+                stp.staple_dropout(self.ctx, stp.STAPLE_BF16, T, D, self.y, self.drops[l],
+                                   b.xs[l + 1], residual=b.xs[l], stream=st)
         # the next step's dedup and first group while the backward runs
         if next_ids is not None:
             rn = self.retr[(self.step_no + 1) % 2]
@@ -235,6 +318,11 @@ class TrainStack:
             r.U_known.synchronize()               # completed long ago: the dedup ran first
             U = int(r.U_host[0])
         dy = dy_top
+        if self.norms is not None:
+            # the stream's gradient dres and, dropped, the top layer's dy
+            dres, dy = dy_top, b.dy[(self.L - 1) % len(b.dy)]
+            stp.staple_dropout(self.ctx, stp.STAPLE_BF16, T, D, dres, self.drops[self.L - 1], dy,
+                               stream=st)
         for l in reversed(range(self.L)):
             w = self.W[l]
             k = l % 2
@@ -253,11 +341,29 @@ class TrainStack:
                                               b.host_dE[l], b.host_unique[l], b.host_U[l],
                                               stream=self.copy)
             b.dE_copied[k].record(self.copy)
-            dx = b.dy[l % len(b.dy)]   # the gradient layer l passes down (layer l-1's dy)
             dwg, dwu, dwd = b.dW[l]
-            stp.staple_ffn_bwd(self.ctx, stp.STAPLE_BF16, T, D, F, dy, b.xs[l], b.z[l], b.dgh,
-                               w.w_gate, w.w_up, dx, dwg, dwu, dwd, stream=st)
-            dy = dx
+            if self.norms is None:
+                dx = b.dy[l % len(b.dy)]   # the gradient layer l passes down (layer l-1's dy)
+                stp.staple_ffn_bwd(self.ctx, stp.STAPLE_BF16, T, D, F, dy, b.xs[l], b.z[l], b.dgh,
+                                   w.w_gate, w.w_up, dx, dwg, dwu, dwd, stream=st)
+                dy = dx
+                continue
+            stp.staple_ffn_bwd(self.ctx, stp.STAPLE_BF16, T, D, F, dy, self.n[l], b.z[l], b.dgh,
+                               w.w_gate, w.w_up, self.dn, dwg, dwu, dwd, stream=st)
+            # through norm_l, joined by the residual's gradient; then, for the
+            # layer below, its dropout
+            dy = b.dy[(l - 1) % len(b.dy)] if l > 0 else None
+            out = self.dstream[l % len(self.dstream)]
+            nw = self.norms[l]
+            dw, db = self.dnorm[l]
+            stp.staple_norm_bwd(self.ctx, stp.STAPLE_BF16, nw.kind, T, D, self.dn, b.xs[l],
+                                self.rstd[l], out, mean=self.mean[l], weight=nw.weight,
+                                dsum_in=dres, drop=self.drops[l - 1] if l > 0 else None, dx=dy,
+                                dw=dw, db=db, workspace=self.nws,
+                                workspace_bytes=self.nws.numel(), stream=st)
+            dres = out
+        if self.norms is not None:
+            self.dx0 = dres
         r.free.record(self.copy)                   # after the last reader (layer 0's copy-out)
         self.host_ready.record(self.copy)
         self.step_no += 1
@@ -272,9 +378,12 @@ class DecodeStack:
     """L augmented layers at decode sizes (T <= 256): one step = dedup,
     group gathers on prefetch streams, the L fused decode layers.  capture()
     records a step into a CUDA graph; replay() runs it for the ids currently
-    in `ids_buf`."""
+    in `ids_buf`.  Layers are LayerWeights or LayerWeightsI8.  norms: one
+    NormWeights per layer, which makes the stack the residual stream
+    x_{l+1} = x_l + FFN_l(norm_l(x_l))."""
 
-    def __init__(self, ctx, weights: list, tables: GroupedTables, T: int, D: int, F: int, V: int):
+    def __init__(self, ctx, weights: list, tables: GroupedTables, T: int, D: int, F: int, V: int,
+                 norms=None):
         import torch
         self.ctx, self.W, self.tables = ctx, weights, tables
         self.T, self.D, self.F, self.V, self.G = T, D, F, V, tables.G
@@ -286,6 +395,14 @@ class DecodeStack:
         self.z = torch.empty((T, F), **bf)
         self.wsb = stp.staple_workspace_bytes(T, D, F)
         self.ws = torch.zeros(self.wsb, dtype=torch.uint8, device="cuda")
+        if any(isinstance(w, LayerWeightsI8) for w in weights):
+            self.wsb8 = stp.staple_ffn_i8_workspace_bytes(T, D, F)
+            self.ws8 = torch.empty(max(self.wsb8, 256), dtype=torch.uint8, device="cuda")
+        self.norms = list(norms) if norms is not None else None
+        if self.norms is not None:
+            assert len(self.norms) == self.L
+            self.n, self.y = torch.empty((T, D), **bf), torch.empty((T, D), **bf)
+            self.no_drop = stp.make_drop(0.0, None)
         self.r = Retrieval(T, F, self.G, tables.n_groups)
         self.pf, self.pf_side = torch.cuda.Stream(), torch.cuda.Stream()
         self.graph = None
@@ -299,14 +416,38 @@ class DecodeStack:
         issue_dedup(self.ctx, r, self.ids_buf, self.V, self.pf, u_to_host=False)
         for gi in range(self.tables.n_groups):
             issue_group(self.ctx, r, self.tables, gi, self.pf, self.pf_side)
+        T, D = self.T, self.D
+        if self.norms is not None:
+            self._norm_fwd(0, self.xs[0], st)
         for l in range(self.L):
             if l % self.G == 0:
                 st.wait_event(r.ready[l // self.G])
-            w = self.W[l]
-            stp.staple_ffn_fwd(self.ctx, stp.STAPLE_BF16, self.T, self.D, self.F, self.xs[l],
-                               r.embed(l), w.w_gate, w.w_up, w.w_down, self.z, self.xs[l + 1],
-                               None, None, self.ws, self.wsb, stream=st)
+            if self.norms is None:
+                self._layer(l, self.xs[l], self.xs[l + 1], st)
+                continue
+            self._layer(l, self.n, self.y, st)
+            if l + 1 < self.L:     # the residual add and the next layer's norm
+                self._norm_fwd(l + 1, self.y, st, residual=self.xs[l], sum=self.xs[l + 1])
+            else:
+                stp.staple_dropout(self.ctx, stp.STAPLE_BF16, T, D, self.y, self.no_drop,
+                                   self.xs[l + 1], residual=self.xs[l], stream=st)
         st.wait_stream(self.pf)                    # join the prefetch streams (graph capture)
+
+    def _norm_fwd(self, l: int, x, st, **kw):
+        nw = self.norms[l]
+        stp.staple_norm_fwd(self.ctx, stp.STAPLE_BF16, nw.kind, self.T, self.D, x, self.n,
+                            weight=nw.weight, bias=nw.bias, eps=nw.eps, stream=st, **kw)
+
+    def _layer(self, l: int, x, y, st):
+        w = self.W[l]
+        if isinstance(w, LayerWeightsI8):
+            stp.staple_ffn_fwd_i8(self.ctx, self.T, self.D, self.F, x, self.r.embed(l), w.w_gate_up,
+                                  w.gate_up_scale, w.w_down, w.down_scale, y, self.ws8, self.wsb8,
+                                  stream=st)
+        else:
+            stp.staple_ffn_fwd(self.ctx, stp.STAPLE_BF16, self.T, self.D, self.F, x,
+                               self.r.embed(l), w.w_gate, w.w_up, w.w_down, self.z, y, None, None,
+                               self.ws, self.wsb, stream=st)
 
     def capture(self, stream, ids_src=None, x_src=None):
         """Record a step into a CUDA graph (kept for replay() and returned).
