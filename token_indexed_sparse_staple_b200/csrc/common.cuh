@@ -41,6 +41,16 @@ __device__ __forceinline__ void wait_prior_kernels() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Let the next kernel of the stream start, if it was launched as a programmatic
+// dependent, as soon as every block of this one has come this far.  Only where
+// that kernel is the library's own and part of the same call: another one
+// might read before it waits (the decode kernel fetches its weights so), and
+// what it reads might be this kernel's output.  After wait_prior_kernels(), so
+// that what it does read early is older than both.
+__device__ __forceinline__ void release_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // bf16 <-> fp32
 // ---------------------------------------------------------------------------

@@ -155,8 +155,10 @@ staple_status launch_dropout(bool bf16, int T, int D, const void* x, const void*
 
 // quant.cu: D is at most kQuantMaxD
 constexpr int kQuantMaxD = 32768;
-staple_status launch_quant_rows(const DeviceInfo& di, bool bf16, int T, int D, const void* x, int8_t* q, float* scale,
-                                cudaStream_t st);
+// (release: the next kernel on the stream is part of the same call and may
+// start early)
+staple_status launch_quant_rows(const DeviceInfo& di, bool bf16, int T, int D, const void* x,
+                                int8_t* q, float* scale, cudaStream_t st, bool release = false);
 
 // z = SiLU(g) (u + E) of an 8-bit layer, straight to 8 bits: gu is [T][2F]
 // (g, then u) or, without u, [T][F]
@@ -169,7 +171,8 @@ staple_status launch_gate_quant(const DeviceInfo& di, int T, int F, const void* 
 constexpr int kI8MaxK = (1 << 17) - 16;
 staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, int K,
                                const int8_t* a, const float* a_scale, const int8_t* b,
-                               const float* b_scale, void* y, int32_t* err, cudaStream_t st);
+                               const float* b_scale, void* y, int32_t* err, cudaStream_t st,
+                               bool release = false);
 
 // simt_f32.cu (fp32 on CUDA cores)
 staple_status f32_ffn_fwd(int T, int D, int F, const float* x, const staple_embed* e,

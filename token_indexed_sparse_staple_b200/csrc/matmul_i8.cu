@@ -78,6 +78,7 @@ struct Params {
   void* y;
   int32_t* err;
   uint64_t wait_ns;
+  bool release;          // the next kernel is part of the same call
   // tiles
   int32_t tiles_t, tiles_n, group_t;
   bool tma_out;
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int ntiles = p.tiles_t * p.tiles_n, kblocks = (p.K + BK - 1) / BK;
   wait_prior_kernels();
+  if (p.release) release_dependents();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -436,6 +438,7 @@ __global__ void __launch_bounds__(kThreads)
     tmem_relinquish();
   }
   if (warp != 0) wait_prior_kernels();
+  if (p.release) release_dependents();
   const int tokens = min(p.tokens, p.T - t0);
   const int channels = min(p.rows, p.N - n0);
   // The scales are fetched now: at the end their latency would count.  One
@@ -678,7 +681,8 @@ staple_status go_split_c(const DeviceInfo& di, const CUtensorMap& w, const CUten
 
 staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, int K,
                                const int8_t* a, const float* a_scale, const int8_t* b,
-                               const float* b_scale, void* y, int32_t* err, cudaStream_t st) {
+                               const float* b_scale, void* y, int32_t* err, cudaStream_t st,
+                               bool release) {
   if (T == 0) return STAPLE_OK;
   // tiles are counted in 32 bits
   if (int64_t(i8::cdiv(T, i8::BM)) * i8::cdiv(N, i8::BN) > INT32_MAX / 2) return STAPLE_EUNSUPPORTED;
@@ -692,6 +696,7 @@ staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, in
   p.y = y;
   p.err = err;
   p.wait_ns = di.wait_ns;
+  p.release = release;
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   CUtensorMap ma, mb, mo;

@@ -41,7 +41,7 @@ struct FwdParams {
   bool rms;
 };
 
-template <bool BF16, int NV, bool VEC, bool DROP>
+template <bool BF16, int NV, RowLayout L, bool DROP>
 // (bf16: 64 registers, so that 32 warps share an SM)
 __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdParams p) {
   __shared__ float red[2][32];
@@ -55,12 +55,11 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
   Raw8<BF16> xr[NV], rr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int g = t + i * p.tpr;
+    const Span e = span<L>(i, t, p.tpr, p.D);
     xr[i] = rr[i] = zero_raw8<BF16>();
-    if (row_ok && g < G) {
-      const int e = g * kGroup, n = min(kGroup, p.D - e);
-      xr[i] = load_raw8<BF16, VEC>(p.x, base + e, n);
-      if (p.res) rr[i] = load_raw8<BF16, VEC>(p.res, base + e, n);
+    if (row_ok && e.n > 0) {
+      xr[i] = load_raw8<BF16, L>(p.x, base, e);
+      if (p.res) rr[i] = load_raw8<BF16, L>(p.res, base, e);
     }
   }
   F2 v[NV][4];
@@ -69,11 +68,11 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
   if (DROP) key = drop_key(p.drop);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int g = t + i * p.tpr;
+    const Span s = span<L>(i, t, p.tpr, p.D);
     float e[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) e[j] = xr[i].get(j);
-    if (DROP) drop8(key, uint64_t(row) * uint64_t(G) + g, p.drop.below, p.drop.scale, e);
+    if (DROP) drop8(key, uint64_t(row) * uint64_t(G) + (t + i * p.tpr), p.drop.below, p.drop.scale, e);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[i][j] = f2(e[2 * j], e[2 * j + 1]);
     if (p.sum) {
@@ -82,8 +81,7 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
 #pragma unroll
       for (int j = 0; j < 4; ++j) f2_get(v[i][j] + pair(rr[i], j), e[2 * j], e[2 * j + 1]);
       const Raw8<BF16> sr = pack_raw8<BF16>(e);
-      if (row_ok && g < G)
-        store_raw8<BF16, VEC>(p.sum, base + g * kGroup, min(kGroup, p.D - g * kGroup), sr);
+      if (row_ok && s.n > 0) store_raw8<BF16, L>(p.sum, base, s, sr);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[i][j] = pair(sr, j);
     }
@@ -103,8 +101,8 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
   const F2 nmean = f2(-mean);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int left = p.D - (t + i * p.tpr) * kGroup;
-    if (VEC ? left > 0 : left >= kGroup) {
+    const int left = span<L>(i, t, p.tpr, p.D).n;
+    if (L == VEC ? left > 0 : left == kGroup) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[i][j] = v[i][j] + nmean;
@@ -113,7 +111,7 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
     } else if (left > 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        // the row's last, partial group: nothing past D counts
+        // eight that the row's end cuts: nothing past D counts
         float lo, hi;
         f2_get(v[i][j] + nmean, lo, hi);
         v[i][j] = f2(2 * j < left ? lo : 0.0f, 2 * j + 1 < left ? hi : 0.0f);
@@ -134,18 +132,17 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
   const F2 rs = f2(rstd);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int g = t + i * p.tpr;
-    if (g >= G) break;
-    const int e = g * kGroup, n = min(kGroup, p.D - e);
+    const Span e = span<L>(i, t, p.tpr, p.D);
+    if (e.n <= 0) break;
     // (a missing weight is ones, a missing bias is zeros)
     Raw8<BF16> w = ones_raw8<BF16>(), b = zero_raw8<BF16>();
-    if (p.w) w = load_raw8<BF16, VEC>(p.w, e, n);
-    if (p.b) b = load_raw8<BF16, VEC>(p.b, e, n);
+    if (p.w) w = load_raw8<BF16, L>(p.w, 0, e);
+    if (p.b) b = load_raw8<BF16, L>(p.b, 0, e);
     float o[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       f2_get(fma2(v[i][j] * rs, pair(w, j), pair(b, j)), o[2 * j], o[2 * j + 1]);
-    store_raw8<BF16, VEC>(p.y, base + e, n, pack_raw8<BF16>(o));
+    store_raw8<BF16, L>(p.y, base, e, pack_raw8<BF16>(o));
   }
 }
 
@@ -165,7 +162,7 @@ struct BwdParams {
 };
 
 // NV groups per thread and row, R rows in flight per thread.
-template <bool BF16, int NV, int R, bool VEC, bool DROP>
+template <bool BF16, int NV, int R, RowLayout L, bool DROP>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
   __shared__ float red[2][2 * R * 32];
   extern __shared__ float s_acc[];   // row groups' dw, db (several row groups per block)
@@ -179,6 +176,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) aw[i][j] = ab[i][j] = 0.0f;
   wait_prior_kernels();
+  if (p.part) release_dependents();
   DropKey key{};
   if (DROP) key = drop_key(p.drop);
   int buf = 0;
@@ -194,12 +192,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
       rs[r] = ok ? p.rstd[row] : 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int g = t + i * p.tpr;
+        const Span e = span<L>(i, t, p.tpr, p.D);
         dyr[r][i] = sr[r][i] = zero_raw8<BF16>();
-        if (ok && g < G) {
-          const int e = g * kGroup, n = min(kGroup, p.D - e);
-          dyr[r][i] = load_raw8<BF16, VEC>(p.dy, row * p.D + e, n);
-          sr[r][i] = load_raw8<BF16, VEC>(p.s, row * p.D + e, n);
+        if (ok && e.n > 0) {
+          dyr[r][i] = load_raw8<BF16, L>(p.dy, row * p.D, e);
+          sr[r][i] = load_raw8<BF16, L>(p.s, row * p.D, e);
         }
       }
     }
@@ -208,17 +205,16 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
     for (int r = 0; r < 2 * R; ++r) c[r] = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int g = t + i * p.tpr;
-      Raw8<BF16> w = zero_raw8<BF16>();
-      if (p.w && g < G)
-        w = load_raw8<BF16, VEC>(p.w, g * kGroup, min(kGroup, p.D - g * kGroup));
+      const Span e = span<L>(i, t, p.tpr, p.D);
+      Raw8<BF16> w = ones_raw8<BF16>();      // (a missing weight)
+      if (p.w && e.n > 0) w = load_raw8<BF16, L>(p.w, 0, e);
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float dy = dyr[r][i].get(j);        // zero past the row's end
           const float xh = (sr[r][i].get(j) - mu[r]) * rs[r];
-          const float gw = p.w ? dy * w.get(j) : dy;
+          const float gw = dy * w.get(j);
           aw[i][j] = fmaf(dy, xh, aw[i][j]);
           ab[i][j] += dy;
           c[2 * r] += gw;
@@ -228,11 +224,10 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
     row_sum(c, p.tpr, red[buf]);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int g = t + i * p.tpr;
-      if (g >= G) break;
-      const int e = g * kGroup, n = min(kGroup, p.D - e);
-      Raw8<BF16> w = zero_raw8<BF16>();
-      if (p.w) w = load_raw8<BF16, VEC>(p.w, e, n);
+      const Span e = span<L>(i, t, p.tpr, p.D);
+      if (e.n <= 0) break;
+      Raw8<BF16> w = ones_raw8<BF16>();
+      if (p.w) w = load_raw8<BF16, L>(p.w, 0, e);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int64_t row = r0 + rg * R + r;
@@ -243,19 +238,19 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
         for (int j = 0; j < 8; ++j) {
           const float dy = dyr[r][i].get(j);
           const float xh = (sr[r][i].get(j) - mu[r]) * rs[r];
-          const float gw = p.w ? dy * w.get(j) : dy;
+          const float gw = dy * w.get(j);
           d[j] = (gw - c1 - xh * c2) * rs[r];
         }
         if (p.dsum_in) {
-          const Raw8<BF16> a = load_raw8<BF16, VEC>(p.dsum_in, row * p.D + e, n);
+          const Raw8<BF16> a = load_raw8<BF16, L>(p.dsum_in, row * p.D, e);
 #pragma unroll
           for (int j = 0; j < 8; ++j) d[j] += a.get(j);
         }
-        if (p.dsum) store_raw8<BF16, VEC>(p.dsum, row * p.D + e, n, pack_raw8<BF16>(d));
+        if (p.dsum) store_raw8<BF16, L>(p.dsum, row * p.D, e, pack_raw8<BF16>(d));
         if (p.dx) {
           // from the fp32 gradient, not from the rounded dsum
-          if (DROP) drop8(key, uint64_t(row) * uint64_t(G) + g, p.drop.below, p.drop.scale, d);
-          store_raw8<BF16, VEC>(p.dx, row * p.D + e, n, pack_raw8<BF16>(d));
+          if (DROP) drop8(key, uint64_t(row) * uint64_t(G) + (t + i * p.tpr), p.drop.below, p.drop.scale, d);
+          store_raw8<BF16, L>(p.dx, row * p.D, e, pack_raw8<BF16>(d));
         }
       }
     }
@@ -270,7 +265,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int e = (t + i * p.tpr) * kGroup + j;
+        const Span sp = span<L>(i, t, p.tpr, p.D);
+        const int e = sp.off + j * sp.step;
         s_acc[(rg * 2 + 0) * cols + e] = aw[i][j];
         s_acc[(rg * 2 + 1) * cols + e] = ab[i][j];
       }
@@ -287,8 +283,9 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int e = (t + i * p.tpr) * kGroup + j;
-      if (e < p.D) {
+      const Span sp = span<L>(i, t, p.tpr, p.D);
+      const int e = sp.off + j * sp.step;
+      if (j < sp.n) {
         out[e] = aw[i][j];
         out[p.D + e] = ab[i][j];
       }
@@ -360,6 +357,7 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
   }
   __syncthreads();
   wait_prior_kernels();
+  if (p.part) release_dependents();
   const int64_t row0 = int64_t(blockIdx.x) * rpb + rg, step = int64_t(gridDim.x) * rpb;
   auto fill = [&](int64_t row, int s) {
     uint8_t* dst = ring + s * stage_bytes;
@@ -388,7 +386,7 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
     for (int i = 0; i < NV; ++i) {
       Raw8<BF16> w = ones_raw8<BF16>();
       if (p.w && t + i * p.tpr < G)
-        w = load_raw8<BF16, true>(p.w, (t + i * p.tpr) * kGroup, kGroup);
+        w = load_raw8<BF16, VEC>(p.w, 0, span<VEC>(i, t, p.tpr, p.D));
 #pragma unroll
       for (int j = 0; j < 4; ++j) ws[i][j] = pair(w, j);
     }
@@ -418,11 +416,12 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int g = t + i * p.tpr;
+      const Span at = span<VEC>(i, t, p.tpr, p.D);
       if (g < G) {
-        const Raw8<BF16> dyr = load_raw8<BF16, true>(src, g * kGroup, kGroup);
-        const Raw8<BF16> sr = load_raw8<BF16, true>(src + rp.row_bytes, g * kGroup, kGroup);
+        const Raw8<BF16> dyr = load_raw8<BF16, VEC>(src, 0, at);
+        const Raw8<BF16> sr = load_raw8<BF16, VEC>(src + rp.row_bytes, 0, at);
         Raw8<BF16> w = ones_raw8<BF16>();
-        if (!KEEP && p.w) w = load_raw8<BF16, true>(p.w, g * kGroup, kGroup);
+        if (!KEEP && p.w) w = load_raw8<BF16, VEC>(p.w, 0, at);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const F2 dy = pair(dyr, j), xh = (pair(sr, j) + nmu) * rs2;
@@ -470,13 +469,14 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
     for (int i = 0; i < NV; ++i) {
       const int g = t + i * p.tpr;
       if (g >= G) break;
+      const Span at = span<VEC>(i, t, p.tpr, p.D);
       Raw8<BF16> dyr, sr, w = ones_raw8<BF16>(), add = zero_raw8<BF16>();
       if (!KEEP) {
-        dyr = load_raw8<BF16, true>(src, g * kGroup, kGroup);
-        sr = load_raw8<BF16, true>(src + rp.row_bytes, g * kGroup, kGroup);
-        if (p.w) w = load_raw8<BF16, true>(p.w, g * kGroup, kGroup);
+        dyr = load_raw8<BF16, VEC>(src, 0, at);
+        sr = load_raw8<BF16, VEC>(src + rp.row_bytes, 0, at);
+        if (p.w) w = load_raw8<BF16, VEC>(p.w, 0, at);
       }
-      if (nt > 2) add = load_raw8<BF16, true>(src + 2 * int64_t(rp.row_bytes), g * kGroup, kGroup);
+      if (nt > 2) add = load_raw8<BF16, VEC>(src + 2 * int64_t(rp.row_bytes), 0, at);
       float d[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -491,12 +491,11 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
         const F2 ds = fma2(fma2(xh, nc2, gw + nc1), rs2, pair(add, j));
         f2_get(ds, d[2 * j], d[2 * j + 1]);
       }
-      const int64_t off = row * p.D + g * kGroup;
-      if (p.dsum) store_raw8<BF16, true>(p.dsum, off, kGroup, pack_raw8<BF16>(d));
+      if (p.dsum) store_raw8<BF16, VEC>(p.dsum, row * p.D, at, pack_raw8<BF16>(d));
       if (p.dx) {
         // from the fp32 gradient, not from the rounded dsum
         if (DROP) drop8(key, uint64_t(row) * uint64_t(G) + g, p.drop.below, p.drop.scale, d);
-        store_raw8<BF16, true>(p.dx, off, kGroup, pack_raw8<BF16>(d));
+        store_raw8<BF16, VEC>(p.dx, row * p.D, at, pack_raw8<BF16>(d));
       }
     }
     if (++st == S) {
@@ -552,9 +551,9 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
 }
 
 // dw[d], db[d] = sums over the blocks of the backward kernel, in block order
-// within each of 8 slices, then over the slices in order.  Block: 32 columns
-// x 8 slices.
-constexpr int kWgCols = 32, kWgSlices = 8;
+// within each of 16 slices, then over the slices in order.  Block: 32 columns
+// x 16 slices.
+constexpr int kWgCols = 32, kWgSlices = 16;
 __global__ void __launch_bounds__(kWgCols* kWgSlices)
     norm_wgrad_kernel(const float* part, int blocks, int D, float* dw, float* db) {
   __shared__ float s[kWgSlices][kWgCols];
@@ -566,7 +565,7 @@ __global__ void __launch_bounds__(kWgCols* kWgSlices)
   float a = 0.0f;
   if (d < D) {
     const float* src = part + int64_t(blockIdx.y) * D + d;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = sl; k < blocks; k += kWgSlices) a += src[int64_t(k) * 2 * D];
   }
   s[sl][cx] = a;
@@ -597,43 +596,59 @@ bool vec_ok(int D, std::initializer_list<const void*> ps) {
   return true;
 }
 
-template <bool BF16, int NV, bool VEC>
-staple_status fwd_go(const FwdParams& p, int grid, int block, cudaStream_t st) {
+template <bool BF16, int NV>
+staple_status fwd_go(const FwdParams& p, bool vec, int grid, int block, cudaStream_t st) {
+  void (*kern)(FwdParams);
+  if (p.drop.rng)
+    kern = vec ? norm_fwd_kernel<BF16, NV, VEC, true> : norm_fwd_kernel<BF16, NV, GROUP, true>;
+  else
+    kern = vec ? norm_fwd_kernel<BF16, NV, VEC, false> : norm_fwd_kernel<BF16, NV, STRIDE, false>;
   cudaError_t ce = cudaSuccess;
   STP_LAUNCH("norm_fwd", st,
-             ce = launch_dependent(p.drop.rng ? norm_fwd_kernel<BF16, NV, VEC, true>
-                                              : norm_fwd_kernel<BF16, NV, VEC, false>,
-                                   dim3(unsigned(grid)), unsigned(block), 0, st, 1, p));
+             ce = launch_dependent(kern, dim3(unsigned(grid)), unsigned(block), 0, st, 1, p));
   return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
-template <bool BF16, bool VEC>
-staple_status fwd_nv(const FwdParams& p, int nv, int grid, int block, cudaStream_t st) {
+template <bool BF16>
+staple_status fwd_nv(const FwdParams& p, int nv, bool vec, int grid, int block, cudaStream_t st) {
   switch (nv) {
-    case 1: return fwd_go<BF16, 1, VEC>(p, grid, block, st);
-    case 2: return fwd_go<BF16, 2, VEC>(p, grid, block, st);
-    default: return fwd_go<BF16, 4, VEC>(p, grid, block, st);
+    case 1: return fwd_go<BF16, 1>(p, vec, grid, block, st);
+    case 2: return fwd_go<BF16, 2>(p, vec, grid, block, st);
+    default: return fwd_go<BF16, 4>(p, vec, grid, block, st);
   }
 }
 
-constexpr int rows_in_flight(bool bf16, int nv) { return nv == 1 ? (bf16 ? 4 : 2) : (nv == 2 && bf16 ? 2 : 1); }
+// Rows in flight per thread of the plain backward kernel: as many as its
+// registers hold, one where there are too few rows to go round the SMs.
+constexpr int rows_in_flight(bool bf16, int nv) {
+  return nv == 1 ? (bf16 ? 4 : 2) : (nv == 2 && bf16 ? 2 : 1);
+}
 
-template <bool BF16, int NV, bool VEC, bool DROP>
-staple_status bwd_go(const BwdParams& p, int grid, int block, size_t smem, cudaStream_t st) {
+template <bool BF16, int NV, int R>
+staple_status bwd_go(const BwdParams& p, bool vec, int grid, int block, size_t smem,
+                     cudaStream_t st) {
+  void (*kern)(BwdParams);
+  if (p.drop.rng)
+    kern = vec ? norm_bwd_kernel<BF16, NV, R, VEC, true> : norm_bwd_kernel<BF16, NV, R, GROUP, true>;
+  else
+    kern = vec ? norm_bwd_kernel<BF16, NV, R, VEC, false>
+               : norm_bwd_kernel<BF16, NV, R, STRIDE, false>;
   cudaError_t ce = cudaSuccess;
   STP_LAUNCH("norm_bwd", st,
-             ce = launch_dependent(norm_bwd_kernel<BF16, NV, rows_in_flight(BF16, NV), VEC, DROP>,
-                                   dim3(unsigned(grid)), unsigned(block), smem, st, 1, p));
+             ce = launch_dependent(kern, dim3(unsigned(grid)), unsigned(block), smem, st, 1, p));
   return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
-template <bool BF16, bool VEC, bool DROP>
-staple_status bwd_nv(const BwdParams& p, int nv, int grid, int block, size_t smem,
+template <bool BF16>
+staple_status bwd_nv(const BwdParams& p, int nv, int R, bool vec, int grid, int block, size_t smem,
                      cudaStream_t st) {
+  if (nv == 1 && R > 1)
+    return bwd_go<BF16, 1, rows_in_flight(BF16, 1)>(p, vec, grid, block, smem, st);
+  if (BF16 && nv == 2 && R > 1) return bwd_go<BF16, 2, 2>(p, vec, grid, block, smem, st);
   switch (nv) {
-    case 1: return bwd_go<BF16, 1, VEC, DROP>(p, grid, block, smem, st);
-    case 2: return bwd_go<BF16, 2, VEC, DROP>(p, grid, block, smem, st);
-    default: return bwd_go<BF16, 4, VEC, DROP>(p, grid, block, smem, st);
+    case 1: return bwd_go<BF16, 1, 1>(p, vec, grid, block, smem, st);
+    case 2: return bwd_go<BF16, 2, 1>(p, vec, grid, block, smem, st);
+    default: return bwd_go<BF16, 4, 1>(p, vec, grid, block, smem, st);
   }
 }
 
@@ -718,22 +733,22 @@ struct DropoutParams {
   int32_t D, G;
 };
 
-template <bool BF16, bool VEC, bool DROP>
+template <bool BF16, RowLayout L, bool DROP>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams p) {
   wait_prior_kernels();
   const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (u >= p.units) return;
   int64_t off = u * kGroup;
-  int n = kGroup;
-  if (!VEC) {
+  Span s{0, 1, kGroup};
+  if (L != VEC) {
     const int64_t row = u / p.G;
     const int e = int(u - row * p.G) * kGroup;
     off = row * p.D + e;
-    n = min(kGroup, p.D - e);
+    s.n = min(kGroup, p.D - e);
   }
-  const Raw8<BF16> xr = load_raw8<BF16, VEC>(p.x, off, n);
+  const Raw8<BF16> xr = load_raw8<BF16, L>(p.x, off, s);
   Raw8<BF16> rr = zero_raw8<BF16>();
-  if (p.res) rr = load_raw8<BF16, VEC>(p.res, off, n);
+  if (p.res) rr = load_raw8<BF16, L>(p.res, off, s);
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = xr.get(j);
@@ -741,16 +756,16 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams p) {
   if (p.res)
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += rr.get(j);
-  store_raw8<BF16, VEC>(p.out, off, n, pack_raw8<BF16>(v));
+  store_raw8<BF16, L>(p.out, off, s, pack_raw8<BF16>(v));
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16, RowLayout L>
 staple_status dropout_go(const DropoutParams& p, cudaStream_t st) {
   const unsigned grid = unsigned((p.units + 255) / 256);
   cudaError_t ce = cudaSuccess;
   STP_LAUNCH("dropout", st,
-             ce = launch_dependent(p.drop.rng ? dropout_kernel<BF16, VEC, true>
-                                              : dropout_kernel<BF16, VEC, false>,
+             ce = launch_dependent(p.drop.rng ? dropout_kernel<BF16, L, true>
+                                              : dropout_kernel<BF16, L, false>,
                                    dim3(grid), 256, 0, st, 1, p));
   return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
@@ -772,10 +787,8 @@ staple_status launch_norm_fwd(const DeviceInfo& di, bool bf16, bool rms, int T, 
   const int rpb = std::max(1, 128 / p.tpr);
   const int grid = cdiv(T, rpb), block = rpb * p.tpr;
   const bool vec = vec_ok(D, {x, res, w, b, sum, y});
-  if (bf16) return vec ? fwd_nv<true, true>(p, nv, grid, block, st)
-                       : fwd_nv<true, false>(p, nv, grid, block, st);
-  return vec ? fwd_nv<false, true>(p, nv, grid, block, st)
-             : fwd_nv<false, false>(p, nv, grid, block, st);
+  return bf16 ? fwd_nv<true>(p, nv, vec, grid, block, st)
+              : fwd_nv<false>(p, nv, vec, grid, block, st);
 }
 
 staple_status launch_norm_bwd(const DeviceInfo& di, bool bf16, bool rms, int T, int D,
@@ -811,20 +824,12 @@ staple_status launch_norm_bwd(const DeviceInfo& di, bool bf16, bool rms, int T, 
     p.tpr = threads_per_row(G, nv);
     const int rpb = std::max(1, 256 / p.tpr);
     const int block = rpb * p.tpr;
-    const int R = rows_in_flight(bf16, nv);
-    grid = std::min(std::min(cdiv(T, int64_t(rpb) * R), kNormMaxBlocks),
-                    di.num_sms * std::max(1, 512 / block));
+    const int blocks = di.num_sms * std::max(1, 768 / block);
+    const int R = T <= int64_t(blocks) * rpb ? 1 : rows_in_flight(bf16, nv);
+    grid = std::min(std::min(cdiv(T, int64_t(rpb) * R), kNormMaxBlocks), blocks);
     const size_t smem = rpb > 1 ? size_t(rpb) * 2 * p.tpr * nv * kGroup * sizeof(float) : 0;
-    if (bf16)
-      r = vec ? (p.drop.rng ? bwd_nv<true, true, true>(p, nv, grid, block, smem, st)
-                            : bwd_nv<true, true, false>(p, nv, grid, block, smem, st))
-              : (p.drop.rng ? bwd_nv<true, false, true>(p, nv, grid, block, smem, st)
-                            : bwd_nv<true, false, false>(p, nv, grid, block, smem, st));
-    else
-      r = vec ? (p.drop.rng ? bwd_nv<false, true, true>(p, nv, grid, block, smem, st)
-                            : bwd_nv<false, true, false>(p, nv, grid, block, smem, st))
-              : (p.drop.rng ? bwd_nv<false, false, true>(p, nv, grid, block, smem, st)
-                            : bwd_nv<false, false, false>(p, nv, grid, block, smem, st));
+    r = bf16 ? bwd_nv<true>(p, nv, R, vec, grid, block, smem, st)
+             : bwd_nv<false>(p, nv, R, vec, grid, block, smem, st);
   }
   if (r != STAPLE_OK || !p.part) return r;
   cudaError_t ce = cudaSuccess;
@@ -840,8 +845,8 @@ staple_status launch_dropout(bool bf16, int T, int D, const void* x, const void*
   DropoutParams p{x, res, out, drop_params(drop), 0, D, groups_of(D)};
   p.units = int64_t(T) * p.G;
   const bool vec = vec_ok(D, {x, res, out});
-  if (bf16) return vec ? dropout_go<true, true>(p, st) : dropout_go<true, false>(p, st);
-  return vec ? dropout_go<false, true>(p, st) : dropout_go<false, false>(p, st);
+  if (bf16) return vec ? dropout_go<true, VEC>(p, st) : dropout_go<true, GROUP>(p, st);
+  return vec ? dropout_go<false, VEC>(p, st) : dropout_go<false, GROUP>(p, st);
 }
 
 }  // namespace stp

@@ -29,6 +29,7 @@ struct QuantParams {
   int8_t* q;
   float* scale;
   int32_t T, D, tpr;
+  bool release;              // the next kernel is part of the same call
   // GATE: x holds g [T][pitch] and, `up` elements further on, u (0: none)
   int64_t pitch;
   int32_t up;
@@ -51,7 +52,7 @@ __device__ __forceinline__ uint32_t q_exact(float x, double scale) {
 
 // GATE: the row is not x but the layer's gated product z = SiLU(g) (u + E),
 // rounded to bf16 as the layer stores it, which thus never goes to memory.
-template <bool BF16, int NV, bool VEC, bool GATE>
+template <bool BF16, int NV, RowLayout L, bool GATE>
 // (bf16: 64 registers, so that 32 warps share an SM)
 __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const QuantParams p) {
   __shared__ uint32_t red[32];
@@ -59,9 +60,9 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
   const int rg = threadIdx.x / p.tpr, t = threadIdx.x - rg * p.tpr;
   const int64_t row = int64_t(blockIdx.x) * rpb + rg;
   const bool row_ok = row < p.T;
-  const int G = (p.D + kGroup - 1) / kGroup;
   const int64_t base = row * p.D;
   wait_prior_kernels();
+  if (p.release) release_dependents();
   const uint16_t* e_row = nullptr;
   if (GATE && row_ok && p.e_base) {
     const int64_t idx = p.e_index[row];
@@ -71,22 +72,21 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
   Raw8<BF16> xr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int g = t + i * p.tpr;
+    const Span s = span<L>(i, t, p.tpr, p.D);
     xr[i] = zero_raw8<BF16>();
-    if (row_ok && g < G) {
+    if (row_ok && s.n > 0) {
       if constexpr (GATE) {
-        const int64_t off = row * p.pitch + g * kGroup;
-        const Raw8<true> gr = load_raw8<true, true>(p.x, off, kGroup);
+        const Raw8<true> gr = load_raw8<true, VEC>(p.x, row * p.pitch, s);
         Raw8<true> ur = zero_raw8<true>(), er = zero_raw8<true>();
-        if (p.up) ur = load_raw8<true, true>(p.x, off + p.up, kGroup);
-        if (e_row) er = load_raw8<true, true>(e_row, g * kGroup, kGroup);
+        if (p.up) ur = load_raw8<true, VEC>(p.x, row * p.pitch + p.up, s);
+        if (e_row) er = load_raw8<true, VEC>(e_row, 0, s);
         float z[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           z[j] = gr.get(j) * sigmoid_f(gr.get(j)) * (ur.get(j) + er.get(j));
         xr[i] = pack_raw8<true>(z);
       } else {
-        xr[i] = load_raw8<BF16, VEC>(p.x, base + g * kGroup, min(kGroup, p.D - g * kGroup));
+        xr[i] = load_raw8<BF16, L>(p.x, base, s);
       }
     }
   }
@@ -130,17 +130,17 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
   const float half = fast ? 0.5f * scale : 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int g = t + i * p.tpr;
-    if (g >= G) break;
+    const Span s = span<L>(i, t, p.tpr, p.D);
+    if (s.n <= 0) break;
     float worst = 0.0f;
     uint32_t b[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const F2 x = pair(xr[i], j);
-      const F2 s = fma2(x, inv, magic);
+      const F2 m = fma2(x, inv, magic);
       float r0, r1, s0, s1;
-      f2_get(fma2(s + nmagic, nscale, x), r0, r1);
-      f2_get(s, s0, s1);
+      f2_get(fma2(m + nmagic, nscale, x), r0, r1);
+      f2_get(m, s0, s1);
       worst = fmaxf(worst, fmaxf(fabsf(r0), fabsf(r1)));
       b[2 * j] = __float_as_uint(s0);
       b[2 * j + 1] = __float_as_uint(s1);
@@ -161,19 +161,18 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
         else hi |= v << (8 * j - 32);
       }
     }
-    int8_t* dst = p.q + base + g * kGroup;
-    if constexpr (VEC) {
+    int8_t* dst = p.q + base + s.off;
+    if constexpr (L == VEC) {
       *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
     } else {
-      const int n = min(kGroup, p.D - g * kGroup);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < n) dst[j] = int8_t((j < 4 ? lo >> (8 * j) : hi >> (8 * j - 32)) & 0xffu);
+        if (j < s.n) dst[j * s.step] = int8_t((j < 4 ? lo >> (8 * j) : hi >> (8 * j - 32)) & 0xffu);
     }
   }
 }
 
-template <bool BF16, bool VEC, bool GATE>
+template <bool BF16, RowLayout L, bool GATE>
 cudaError_t go(const DeviceInfo& di, QuantParams p, cudaStream_t st) {
   // few rows: as many threads per row as there are groups; many: up to eight
   // groups per thread, whose loads are in flight together and whose maximum
@@ -188,19 +187,20 @@ cudaError_t go(const DeviceInfo& di, QuantParams p, cudaStream_t st) {
   const dim3 grid(unsigned((int64_t(p.T) + rpb - 1) / rpb));
   const unsigned block = unsigned(rpb * p.tpr);
   switch (nv) {
-    case 1: return launch_dependent(quant_rows_kernel<BF16, 1, VEC, GATE>, grid, block, 0, st, 1, p);
-    case 2: return launch_dependent(quant_rows_kernel<BF16, 2, VEC, GATE>, grid, block, 0, st, 1, p);
-    case 4: return launch_dependent(quant_rows_kernel<BF16, 4, VEC, GATE>, grid, block, 0, st, 1, p);
-    default: return launch_dependent(quant_rows_kernel<BF16, 8, VEC, GATE>, grid, block, 0, st, 1, p);
+    case 1: return launch_dependent(quant_rows_kernel<BF16, 1, L, GATE>, grid, block, 0, st, 1, p);
+    case 2: return launch_dependent(quant_rows_kernel<BF16, 2, L, GATE>, grid, block, 0, st, 1, p);
+    case 4: return launch_dependent(quant_rows_kernel<BF16, 4, L, GATE>, grid, block, 0, st, 1, p);
+    default: return launch_dependent(quant_rows_kernel<BF16, 8, L, GATE>, grid, block, 0, st, 1, p);
   }
 }
 
 }  // namespace
 
 staple_status launch_quant_rows(const DeviceInfo& di, bool bf16, int T, int D, const void* x,
-                                int8_t* q, float* scale, cudaStream_t st) {
+                                int8_t* q, float* scale, cudaStream_t st, bool release) {
   if (T == 0) return STAPLE_OK;
   QuantParams p{};
+  p.release = release;
   p.x = x;
   p.q = q;
   p.scale = scale;
@@ -210,8 +210,8 @@ staple_status launch_quant_rows(const DeviceInfo& di, bool bf16, int T, int D, c
                    (reinterpret_cast<uintptr_t>(q) & 7u) == 0;
   cudaError_t ce = cudaSuccess;
   STP_LAUNCH("quant_rows", st,
-             ce = bf16 ? (vec ? go<true, true, false>(di, p, st) : go<true, false, false>(di, p, st))
-                       : (vec ? go<false, true, false>(di, p, st) : go<false, false, false>(di, p, st)));
+             ce = bf16 ? (vec ? go<true, VEC, false>(di, p, st) : go<true, STRIDE, false>(di, p, st))
+                       : (vec ? go<false, VEC, false>(di, p, st) : go<false, STRIDE, false>(di, p, st)));
   return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
@@ -220,6 +220,7 @@ staple_status launch_gate_quant(const DeviceInfo& di, int T, int F, const void* 
                                 cudaStream_t st) {
   if (T == 0) return STAPLE_OK;
   QuantParams p{};
+  p.release = true;
   p.x = gu;
   p.q = q;
   p.scale = scale;
@@ -235,7 +236,7 @@ staple_status launch_gate_quant(const DeviceInfo& di, int T, int F, const void* 
   }
   p.err = err;
   cudaError_t ce = cudaSuccess;
-  STP_LAUNCH("gate_quant", st, ce = (go<true, true, true>(di, p, st)));
+  STP_LAUNCH("gate_quant", st, ce = (go<true, VEC, true>(di, p, st)));
   return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 

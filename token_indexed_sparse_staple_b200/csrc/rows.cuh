@@ -20,13 +20,37 @@ struct Raw8 {
   }
 };
 
-// Load n <= 8 elements from element offset `off`; the rest are zero.  VEC:
-// n == 8 and the address is 16-byte aligned.  Plain (coherent) loads: the
-// outputs of these kernels may share the inputs' memory.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ Raw8<BF16> load_raw8(const void* base, int64_t off, int n) {
+// How a thread's eight elements lie in a row.  VEC: side by side, on a 16-byte
+// boundary, all within the row.  GROUP: side by side, element by element.
+// STRIDE: one from each of eight runs of tpr elements, so that a warp's loads
+// are side by side; rows of an odd length take it unless dropout needs the
+// groups of eight that share a draw.
+enum RowLayout { VEC, GROUP, STRIDE };
+
+// The elements of thread t's i-th eight: off + j * step for j < n, where n may
+// be zero or less.
+struct Span {
+  int off, step, n;
+};
+template <RowLayout L>
+__device__ __forceinline__ Span span(int i, int t, int tpr, int D) {
+  if constexpr (L == STRIDE) {
+    const int off = i * kGroup * tpr + t;
+    return Span{off, tpr, off < D ? min(kGroup, (D - off + tpr - 1) / tpr) : 0};
+  } else {
+    const int off = (t + i * tpr) * kGroup;
+    return Span{off, 1, min(kGroup, D - off)};
+  }
+}
+
+// Load the n <= 8 elements base[row + off + j * step]; the rest are zero.
+// Plain (coherent) loads: the outputs of these kernels may share the inputs'
+// memory.
+template <bool BF16, RowLayout L>
+__device__ __forceinline__ Raw8<BF16> load_raw8(const void* base, int64_t row, const Span& s) {
   Raw8<BF16> r;
-  if constexpr (VEC) {
+  const int64_t off = row + s.off;
+  if constexpr (L == VEC) {
     if constexpr (BF16) {
       const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
       r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
@@ -38,16 +62,18 @@ __device__ __forceinline__ Raw8<BF16> load_raw8(const void* base, int64_t off, i
     }
   } else if constexpr (BF16) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + off;
+    const int step = L == GROUP ? 1 : s.step;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = 2 * i < n ? p[2 * i] : 0u;
-      const uint32_t hi = 2 * i + 1 < n ? p[2 * i + 1] : 0u;
+      const uint32_t lo = 2 * i < s.n ? p[2 * i * step] : 0u;
+      const uint32_t hi = 2 * i + 1 < s.n ? p[(2 * i + 1) * step] : 0u;
       r.w[i] = lo | (hi << 16);
     }
   } else {
     const uint32_t* p = static_cast<const uint32_t*>(base) + off;
+    const int step = L == GROUP ? 1 : s.step;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.w[i] = i < n ? p[i] : 0u;
+    for (int i = 0; i < 8; ++i) r.w[i] = i < s.n ? p[i * step] : 0u;
   }
   return r;
 }
@@ -83,9 +109,11 @@ __device__ __forceinline__ Raw8<BF16> pack_raw8(const float (&v)[8]) {
   return r;
 }
 
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void store_raw8(void* base, int64_t off, int n, const Raw8<BF16>& r) {
-  if constexpr (VEC) {
+template <bool BF16, RowLayout L>
+__device__ __forceinline__ void store_raw8(void* base, int64_t row, const Span& s,
+                                           const Raw8<BF16>& r) {
+  const int64_t off = row + s.off;
+  if constexpr (L == VEC) {
     if constexpr (BF16) {
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + off) =
           make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
@@ -96,14 +124,16 @@ __device__ __forceinline__ void store_raw8(void* base, int64_t off, int n, const
     }
   } else if constexpr (BF16) {
     uint16_t* p = static_cast<uint16_t*>(base) + off;
+    const int step = L == GROUP ? 1 : s.step;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = uint16_t((i & 1) ? r.w[i >> 1] >> 16 : r.w[i >> 1] & 0xffffu);
+      if (i < s.n) p[i * step] = uint16_t((i & 1) ? r.w[i >> 1] >> 16 : r.w[i >> 1] & 0xffffu);
   } else {
     uint32_t* p = static_cast<uint32_t*>(base) + off;
+    const int step = L == GROUP ? 1 : s.step;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = r.w[i];
+      if (i < s.n) p[i * step] = r.w[i];
   }
 }
 
