@@ -50,6 +50,37 @@ __device__ __forceinline__ uint32_t q_exact(float x, double scale) {
   return uint32_t(int(d)) & 0xffu;
 }
 
+// A group's eight bytes.
+template <RowLayout L>
+__device__ __forceinline__ void store8(int8_t* row, const Span& s, uint32_t lo, uint32_t hi) {
+  int8_t* dst = row + s.off;
+  if constexpr (L == VEC) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < s.n) dst[j * s.step] = int8_t((j < 4 ? lo >> (8 * j) : hi >> (8 * j - 32)) & 0xffu);
+  }
+}
+
+__device__ __forceinline__ float gated(float g, float u, float e) {
+  return g * sigmoid_f(g) * (u + e);
+}
+
+// One element of a row, as the kernel below loads it.
+template <bool BF16, bool GATE>
+__device__ __forceinline__ float element(const QuantParams& p, int64_t row, int d,
+                                         const uint16_t* e_row) {
+  const uint16_t* h = static_cast<const uint16_t*>(p.x);
+  if constexpr (GATE) {
+    const uint16_t* g = h + row * p.pitch + d;
+    const float z = gated(bf2f(g[0]), p.up ? bf2f(g[p.up]) : 0.0f, e_row ? bf2f(e_row[d]) : 0.0f);
+    return bf_lo(pack_bf2(z, 0.0f));
+  } else {
+    return BF16 ? bf2f(h[row * p.D + d]) : static_cast<const float*>(p.x)[row * p.D + d];
+  }
+}
+
 // GATE: the row is not x but the layer's gated product z = SiLU(g) (u + E),
 // rounded to bf16 as the layer stores it, which thus never goes to memory.
 template <bool BF16, int NV, RowLayout L, bool GATE>
@@ -82,8 +113,7 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
         if (e_row) er = load_raw8<true, VEC>(e_row, 0, s);
         float z[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          z[j] = gr.get(j) * sigmoid_f(gr.get(j)) * (ur.get(j) + er.get(j));
+        for (int j = 0; j < 8; ++j) z[j] = gated(gr.get(j), ur.get(j), er.get(j));
         xr[i] = pack_raw8<true>(z);
       } else {
         xr[i] = load_raw8<BF16, L>(p.x, base, s);
@@ -128,6 +158,7 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
   const F2 magic = f2(kRintMagic), nmagic = f2(-kRintMagic);
   const bool fast = finite && amax >= kTiny;
   const float half = fast ? 0.5f * scale : 0.0f;
+  uint32_t redo = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const Span s = span<L>(i, t, p.tpr, p.D);
@@ -146,29 +177,29 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
       b[2 * j + 1] = __float_as_uint(s1);
     }
     // the low bytes of four words
-    uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-    if (!(worst < half)) {
-      lo = hi = 0;
+    const uint32_t lo =
+        __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    const uint32_t hi =
+        __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    store8<L>(p.q + base, s, lo, hi);
+    if (!(worst < half)) redo |= 1u << i;
+  }
+  // groups that need the division (and all of a row that is tiny, zero or not
+  // finite), behind the others so that no branch stands between their loads
+  // and stores; their elements are read again
+  while (redo) {
+    const int i = __ffs(int(redo)) - 1;
+    redo &= redo - 1;
+    const Span s = span<L>(i, t, p.tpr, p.D);
+    uint32_t lo = 0, hi = 0;
 #pragma unroll 1
-      for (int j = 0; j < 8; ++j) {
-        float x = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k == j) x = xr[i].get(k);
-        const uint32_t v = finite && scale > 0.0f ? q_exact(x, double(scale)) : 0u;
-        if (j < 4) lo |= v << (8 * j);
-        else hi |= v << (8 * j - 32);
-      }
+    for (int j = 0; j < s.n; ++j) {
+      const float x = element<BF16, GATE>(p, row, s.off + j * s.step, e_row);
+      const uint32_t v = finite && scale > 0.0f ? q_exact(x, double(scale)) : 0u;
+      if (j < 4) lo |= v << (8 * j);
+      else hi |= v << (8 * j - 32);
     }
-    int8_t* dst = p.q + base + s.off;
-    if constexpr (L == VEC) {
-      *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < s.n) dst[j * s.step] = int8_t((j < 4 ? lo >> (8 * j) : hi >> (8 * j - 32)) & 0xffu);
-    }
+    store8<L>(p.q + base, s, lo, hi);
   }
 }
 
