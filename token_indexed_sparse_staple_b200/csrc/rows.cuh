@@ -222,13 +222,11 @@ __device__ __forceinline__ uint4 philox(const DropKey& k, uint64_t n) {
   return make_uint4(c0, c1, c2, c3);
 }
 
-// v[i] = kept ? v[i] * scale : 0 for the eight elements of group n.  A dropped
+// v[i] = kept ? v[i] * scale : 0 for eight elements with the draws u.  A dropped
 // element is zero whatever it held (an infinity or a NaN included).  A draw in
 // the high half is compared without taking it out of its word; thr = 2^16
 // makes `below` the largest word, which no word exceeds.
-__device__ __forceinline__ void drop8(const DropKey& k, uint64_t n, uint32_t below, float scale,
-                                      float (&v)[8]) {
-  const uint4 u = philox(k, n);
+__device__ __forceinline__ void drop8(const uint4& u, uint32_t below, float scale, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
