@@ -11,10 +11,12 @@
 // one of storage.
 //
 // Two kernels:
-//  * tiles: many tokens.  Tokens take the MMA's M side, 128 x 256 outputs per
-//    tile, persistent blocks, two accumulators in tensor memory so that a
-//    tile's epilogue runs beside the next tile's products.  Bound by the
-//    tensor cores.
+//  * tiles: many tokens.  Tokens take the MMA's M side; a pair of SMs shares a
+//    256 x 256 tile (cta_group::2), each holding half of either operand, so
+//    that an operand byte is fetched from L2 and read from shared memory once
+//    for twice the products of a 128 x 256 tile.  Persistent pairs, two
+//    accumulators in tensor memory so that a tile's epilogue runs beside the
+//    next tile's products.  Bound by the tensor cores.
 //  * split: few tiles (decode, or narrow outputs).  The weights take the M
 //    side and up to 256 tokens the N side, so a block is a stream of weights;
 //    bound by HBM.  Where k is split too, the blocks of a cluster add their
@@ -46,19 +48,76 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, signed 8-bit inputs, int32
-// accumulator; K = 32 per instruction.  The whole warp calls it with the same
-// operands and the elected lane issues it: a loop that only one lane runs
+// accumulator; K = 32 per instruction.  PAIR: one instruction over the shared
+// and tensor memories of two SMs, M = 256.  The whole warp calls it with the
+// same operands and the elected lane issues it: a loop that only one lane runs
 // moves every operand into the uniform registers anew, which took 100 cycles
 // per instruction here, more than a 128 x 64 x 32 product takes (49).
+template <bool PAIR>
 __device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                      uint32_t idesc, uint32_t accumulate, uint32_t elected) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+
+// Every thread of every block of the cluster; shared-memory writes before it
+// are seen after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
+                   "memory");
+}
+// The cluster address of this block's shared-memory word in block `rank`.
+__device__ __forceinline__ uint32_t map_peer(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+
+// The pair's forms of the wrappers in common.cuh.  A load lands in the shared
+// memory of the block that issues it and counts on a barrier that may be the
+// other block's; a commit arrives on the same barrier of both blocks.
+__device__ __forceinline__ void pair_load_2d(const CUtensorMap* map, uint32_t bar, void* dst,
+                                             int32_t c0, int32_t c1) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
+}
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(uint16_t(3))
+      : "memory");
+}
+__device__ __forceinline__ void pair_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
 }
 
 // Instruction descriptor for kind::i8: int32 accumulator, signed A and B, both
@@ -92,8 +151,9 @@ struct Params {
 
 // ---------------------------------------------------------------- tiles
 
-constexpr int BM = 128, BN = 256, STAGES = 4, kThreads = 192;
-constexpr int A_STAGE = BM * BK, B_STAGE = BN * BK, STAGE_BYTES = A_STAGE + B_STAGE;
+constexpr int BM = 128, BN = 256, STAGES = 6, kThreads = 192;
+// per block and stage: 128 of the pair's 256 tokens and 128 of its 256 channels
+constexpr int HALF_STAGE = 128 * BK, STAGE_BYTES = 2 * HALF_STAGE;
 // One warp's staged 32 x 32 outputs: two blocks of bf16, or one of fp32.
 constexpr int kOutBox = 32 * 32 * 4;
 // One block per SM, whatever the output type: two would not share the 512
@@ -111,6 +171,8 @@ __device__ __forceinline__ void tile_coords(int t, const Params& p, int& mb, int
   nb = r / rows;
 }
 
+// Blocks 2i and 2i + 1 are a pair; the even one leads: it waits for both
+// blocks' loads and issues the products.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     tiles_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -118,17 +180,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint8_t* sA = smem;
-  uint8_t* sB = smem + STAGES * A_STAGE;
-  uint8_t* s_out = sB + STAGES * B_STAGE;
+  uint8_t* sB = smem + STAGES * HALF_STAGE;
+  uint8_t* s_out = sB + STAGES * HALF_STAGE;
   float* s_scale = reinterpret_cast<float*>(s_out + 4 * kOutBox);   // [4 warps][256]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + 4 * BN);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + 4 * BN);   // the leader's are used
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 2;
+  uint64_t* tempty = tfull + 2;                                     // the leader's are used
   uint64_t* dbar = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dbar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(blockIdx.x & 1u);
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -136,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4);
+      mbar_init(&tempty[b], 8);      // four epilogue warps in either block
     }
     mbar_init(dbar, 1);
     *abort_flag = 0;
@@ -144,15 +207,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
-  }
+  if (warp == 1) pair_tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();      // the other block's barriers are set up too
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int ntiles = p.tiles_t * p.tiles_n, kblocks = (p.K + BK - 1) / BK;
+  const int first = int(blockIdx.x >> 1), step = int(gridDim.x >> 1);
   wait_prior_kernels();
   if (p.release) release_dependents();
 
@@ -161,17 +223,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      for (int t = first; t < ntiles && ok; t += step) {
         int mb, nb;
         tile_coords(t, p, mb, nb);
+        const int m0 = mb * 2 * BM + rank * BM, n0 = nb * BN + rank * 128;
         for (int kb = 0; kb < kblocks; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, p.wait_ns)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
-          tma_load_2d(&tmA, &full[stage], sA + stage * A_STAGE, kb * BK, mb * BM);
-          tma_load_2d(&tmB, &full[stage], sB + stage * B_STAGE, kb * BK, nb * BN);
+          // (the other block's bytes may be counted before this: the phase
+          // cannot end without the arrival)
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
+          const uint32_t bar = map_peer(smem_u32(&full[stage]), 0);
+          pair_load_2d(&tmA, bar, sA + stage * HALF_STAGE, kb * BK, m0);
+          pair_load_2d(&tmB, bar, sB + stage * HALF_STAGE, kb * BK, n0);
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -179,53 +245,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      drain_ring(full, STAGES, stage, phase, issued);
-    }
-  } else if (warp == 1) {
-    const uint32_t elected = elect_one();
-    const uint64_t a0 = sw128_desc(smem_u32(sA), 16, 1024), b0 = sw128_desc(smem_u32(sB), 16, 1024);
-    int stage = 0, iter = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x, ++iter) {
-      const int buf = iter & 1;
-      ok = mbar_wait(&tempty[buf], (uint32_t(iter >> 1) & 1) ^ 1, abort_flag, p.err, p.wait_ns);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      const uint32_t dacc = tmem_base + uint32_t(buf * BN);
-      for (int kb = 0; kb < kblocks; ++kb) {
-        ok = mbar_wait(&full[stage], phase, abort_flag, p.err, p.wait_ns);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t a = a0 + uint64_t(stage * (A_STAGE >> 4));
-        const uint64_t b = b0 + uint64_t(stage * (B_STAGE >> 4));
-#pragma unroll
-        for (int k = 0; k < BK / 32; ++k)   // 32 bytes further on: 2 in the address field
-          umma(dacc, a + 2 * k, b + 2 * k, idesc(BM, BN), (kb | k) ? 1u : 0u, elected);
-        if (elected) umma_commit(&empty[stage]);
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
+      if (rank == 0) {
+        drain_ring(full, STAGES, stage, phase, issued);
+      } else if (!ok) {
+        // the leader counts this block's loads; after a wait that ran out,
+        // give those in flight the time to land
+        for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < kDrainNs;) {
         }
       }
-      if (ok && elected) umma_commit(&tfull[buf]);
     }
-    if (elected) umma_commit(dbar);
-    __syncwarp();
-    mbar_drain(dbar, 0);
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t elected = elect_one();
+      const uint64_t a0 = sw128_desc(smem_u32(sA), 16, 1024);
+      const uint64_t b0 = sw128_desc(smem_u32(sB), 16, 1024);
+      int stage = 0, iter = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; t < ntiles && ok; t += step, ++iter) {
+        const int buf = iter & 1;
+        ok = mbar_wait(&tempty[buf], (uint32_t(iter >> 1) & 1) ^ 1, abort_flag, p.err, p.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const uint32_t dacc = tmem_base + uint32_t(buf * BN);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          ok = mbar_wait(&full[stage], phase, abort_flag, p.err, p.wait_ns);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t a = a0 + uint64_t(stage * (HALF_STAGE >> 4));
+          const uint64_t b = b0 + uint64_t(stage * (HALF_STAGE >> 4));
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)   // 32 bytes further on: 2 in the address field
+            umma<true>(dacc, a + 2 * k, b + 2 * k, idesc(2 * BM, BN), (kb | k) ? 1u : 0u, elected);
+          if (elected) pair_commit(&empty[stage]);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok && elected) pair_commit(&tfull[buf]);
+      }
+      if (elected) pair_commit(dbar);
+      __syncwarp();
+      mbar_drain(dbar, 0);
+    }
   } else {
     const int q = warp & 3;
     uint8_t* box = s_out + q * kOutBox;
     float* scales = s_scale + q * BN;      // the tile's channel scales, a copy per warp
     int iter = 0;
-    for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++iter) {
+    const uint32_t free_bar[2] = {map_peer(smem_u32(&tempty[0]), 0), map_peer(smem_u32(&tempty[1]), 0)};
+    for (int t = first; t < ntiles; t += step, ++iter) {
       const int buf = iter & 1;
       int mb, nb;
       tile_coords(t, p, mb, nb);
-      const int m0 = mb * BM + q * 32, m = m0 + lane;
+      const int m0 = mb * 2 * BM + rank * BM + q * 32, m = m0 + lane;
       const float sa = m < p.T ? __ldg(p.a_scale + m) : 0.0f;
 #pragma unroll
       for (int i = 0; i < BN / 32; ++i) {
@@ -301,17 +378,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[buf]);
+      if (lane == 0) pair_arrive(free_bar[buf]);
     }
     if (p.tma_out && lane == 0) bulk_wait0();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();      // the products, which read both blocks' memory, are over
   tc_fence_after();
-  if (warp == 1) {
-    __syncwarp();
-    tmem_dealloc(tmem_base, 512);
-  }
+  if (warp == 1) pair_tmem_dealloc(tmem_base, 512);
+  cluster_sync();
 }
 
 // ---------------------------------------------------------------- split
@@ -324,14 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kUnit = 2 * BK;               // 256 bytes of each row per stage
 constexpr int kMaxTokens = 256, kMaxStages = 24;
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
-                   "memory");
-}
 __device__ __forceinline__ int4 ld_cluster(uint32_t addr, uint32_t rank) {
-  uint32_t a;
+  const uint32_t a = map_peer(addr, rank);
   int4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(a));
@@ -488,7 +559,7 @@ __global__ void __launch_bounds__(kThreads)
       const uint64_t w = d0 + uint64_t(uint32_t(stage * stage_bytes) >> 4), x = w + 2 * dw;
 #pragma unroll
       for (int k = 0; k < 8; ++k)   // 32 bytes further on: 2 in the address field
-        umma(tmem_base, w + (k >> 2) * dw + (k & 3) * 2, x + (k >> 2) * dx + (k & 3) * 2, id,
+        umma<false>(tmem_base, w + (k >> 2) * dw + (k & 3) * 2, x + (k >> 2) * dx + (k & 3) * 2, id,
              (i | k) ? 1u : 0u, elected);
       if (elected) umma_commit(&empty[stage]);
       if (++stage == S) {
@@ -644,12 +715,12 @@ staple_status go_tiles(const DeviceInfo& di, const CUtensorMap& a, const CUtenso
   auto kern = i8::tiles_kernel<BF16>;
   if (!opt_in(kern, i8::kTilesSmem, di.device, done)) return STAPLE_ECUDA;
   const int ntiles = p.tiles_t * p.tiles_n;
-  const int avail = std::max(1, di.num_sms - di.sm_reserve);
-  const int per = i8::cdiv(ntiles, avail);
+  const int pairs = std::max(1, (di.num_sms - di.sm_reserve) / 2);
+  const int per = i8::cdiv(ntiles, pairs);
   cudaError_t ce = cudaSuccess;
   STP_LAUNCH("matmul_i8", st,
-             ce = launch_dependent(kern, dim3(unsigned(i8::cdiv(ntiles, per))), i8::kThreads,
-                                   i8::kTilesSmem, st, 1, a, b, o, p));
+             ce = launch_dependent(kern, dim3(2 * unsigned(i8::cdiv(ntiles, per))), i8::kThreads,
+                                   i8::kTilesSmem, st, 2, a, b, o, p));
   return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
 }
 
@@ -685,7 +756,8 @@ staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, in
                                bool release) {
   if (T == 0) return STAPLE_OK;
   // tiles are counted in 32 bits
-  if (int64_t(i8::cdiv(T, i8::BM)) * i8::cdiv(N, i8::BN) > INT32_MAX / 2) return STAPLE_EUNSUPPORTED;
+  if (int64_t(i8::cdiv(T, 2 * i8::BM)) * i8::cdiv(N, i8::BN) > INT32_MAX / 2)
+    return STAPLE_EUNSUPPORTED;
   const int es = bf16 ? 2 : 4;
   i8::Params p{};
   p.T = T;
@@ -700,13 +772,13 @@ staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, in
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   CUtensorMap ma, mb, mo;
-  p.tiles_t = i8::cdiv(T, i8::BM);
+  p.tiles_t = i8::cdiv(T, 2 * i8::BM);
   p.tiles_n = i8::cdiv(N, i8::BN);
-  if (T > i8::kMaxTokens && int64_t(p.tiles_t) * p.tiles_n >= di.num_sms) {
-    p.group_t = 16;
+  if (T > i8::kMaxTokens && int64_t(p.tiles_t) * p.tiles_n >= di.num_sms / 2) {
+    p.group_t = 8;
     p.tma_out = (int64_t(N) * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
     if (!tensor_map_2d(&ma, u8, 1, a, K, T, K, i8::BK, i8::BM, sw) ||
-        !tensor_map_2d(&mb, u8, 1, b, K, N, K, i8::BK, i8::BN, sw))
+        !tensor_map_2d(&mb, u8, 1, b, K, N, K, i8::BK, 128, sw))
       return STAPLE_ECUDA;
     mo = ma;
     if (p.tma_out &&
