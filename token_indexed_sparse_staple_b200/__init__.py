@@ -44,13 +44,12 @@ def lib():
 
 def _p(x) -> int | None:
     """Address of a tensor / array / raw int (None -> NULL)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
-    if isinstance(x, np.ndarray):
-        return x.ctypes.data
-    return x.data_ptr()
+    try:
+        return x.data_ptr()     # tensors first: a call has up to ten of them
+    except AttributeError:
+        return x.ctypes.data if isinstance(x, np.ndarray) else int(x)
 
 
 def _stream(s) -> int | None:
