@@ -502,7 +502,8 @@ staple_status staple_dropout(staple_context* ctx, staple_dtype dtype, int32_t T,
  * q[t][d] = x[t][d] / scale[t] rounded to the nearest integer, ties to even
  * (the exact quotient is rounded), within [-127, 127].  A row of zeros has
  * scale 0 and q 0.  A row that holds an infinity or a NaN has that as its
- * scale (NaN before infinity) and q 0, so products with it are NaN.
+ * scale (NaN before infinity) and q 0, so products with it are NaN.  q must not
+ * overlap x.
  *   x   [T][D] (dtype), D at most 32768 (STAPLE_EUNSUPPORTED beyond)
  *   q   out int8 [T][D];  scale  out fp32 [T]
  * The same call quantises a weight [out][in] with one scale per output

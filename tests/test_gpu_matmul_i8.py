@@ -185,3 +185,27 @@ def test_quantised_product_of_float_rows(stp, ctx):
 
 def test_an_empty_batch(stp, ctx):
     stp.staple_matmul_i8(ctx, stp.STAPLE_BF16, 0, 8, 16, None, None, None, None, None)
+
+
+@pytest.mark.parametrize("T, N", [(300, 9472), (3, 8192), (64, 200)])
+def test_a_wait_that_runs_out_is_reported_and_the_context_recovers(stp, ctx, T, N):
+    """The longest K makes the first sum take tens of microseconds at least (a
+    pair of SMs 280, a block of a full split 150, a block of a cluster of 8
+    about 20), so a limit of 10 us runs out in the first wait for an
+    accumulator; the same context then computes the product."""
+    import torch
+    a, sa, b, sb = operands(T, N, 131056, 7)
+    assert stp.staple_get_error(ctx) == 0
+    stp.staple_set_wait_limit(ctx, 10_000)
+    try:
+        run(stp, ctx, "bf16", a, sa, b, sb)
+        err = stp.staple_get_error(ctx)
+    finally:
+        stp.staple_set_wait_limit(ctx, 4_000_000_000)
+    assert err == stp.STAPLE_ETIMEOUT, stp.staple_status_string(err)
+    y = run(stp, ctx, "f32", a, sa, b, sb)
+    assert stp.staple_get_error(ctx) == 0
+    rows = torch.arange(0, T, max(1, T // 5), device="cuda")      # some tokens are enough
+    want = ((a[rows].double() @ b.double().t()) * sa[rows].double()[:, None]
+            * sb.double()[None, :])
+    assert ((y[rows].double() - want).abs() <= TOL["f32"] * want.abs()).all()

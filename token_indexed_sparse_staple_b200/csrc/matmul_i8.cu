@@ -690,8 +690,11 @@ SplitPlan plan_split(int num_sms, int N, int units, int tokens, int tiles_t, int
     // block that waits for columns could wait for a cluster whose other blocks
     // wait for it: so no block takes a smaller part of the SM's 228 KB than of
     // its columns, and none fits beside a tiled GEMM block (at least 193.25 KB
-    // and all columns).
-    const int share = std::max(int(int64_t(cols) * 228 * 1024 / 512) - 1024, 36 * 1024);
+    // and all columns).  A cluster's blocks do not fit beside a block of the
+    // decode kernel either (147 KB or more, all columns): its blocks wait for
+    // one another as a cluster's do, and the two could wait in a circle.
+    const int share = std::max(int(int64_t(cols) * 228 * 1024 / 512) - 1024,
+                               (c > 1 ? 84 : 36) * 1024);
     best_us = us;
     best = SplitPlan{c, rows, stages, std::max(want, share)};
   }

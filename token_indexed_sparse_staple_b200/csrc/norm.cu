@@ -362,7 +362,9 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
   wait_prior_kernels();
   if (p.part) release_dependents();
   const int64_t row0 = int64_t(blockIdx.x) * rpb + rg, step = int64_t(gridDim.x) * rpb;
+  int issued = 0;      // (the filling thread's) fills so far, in ring order
   auto fill = [&](int64_t row, int s) {
+    ++issued;
     uint8_t* dst = ring + s * stage_bytes;
     const int64_t off = row * rp.row_bytes;
     mbar_arrive_expect_tx(&full[s], uint32_t(stage_bytes));
@@ -410,7 +412,8 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
     const float mu = mu_next, rs = rs_next;
     fetch(row + step);
     // After a wait that ran out the group goes on with what the stage holds
-    // (its outputs are then undefined); the flag ends every later wait.
+    // (its outputs are then undefined); the flag ends every later wait, and no
+    // stage is filled again.
     mbar_wait(&full[st], ph, abort, rp.err, rp.wait_ns);
     const uint8_t* src = ring + st * stage_bytes;
     F2 c1 = f2(0.0f), c2 = f2(0.0f);
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
     }
     // row - step is behind every thread of the group: its stage takes the
     // row S - 1 steps ahead of this one
-    if (t == 0 && row != row0 && row + (S - 1) * step < p.T)
+    if (t == 0 && row != row0 && row + (S - 1) * step < p.T && !*abort)
       fill(row + (S - 1) * step, st == 0 ? S - 1 : st - 1);
     // the row's draws, generated side by side: one chain of ten rounds after
     // the other would leave the warp waiting for its own results
@@ -514,8 +517,7 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
   }
   // every fill was waited for above, unless a wait ran out: then let the
   // copies in flight land before the shared memory goes away
-  if (*abort && t == 0)
-    for (int s = 0; s < S; ++s) mbar_drain(&full[s], s < st ? ph : ph ^ 1);
+  if (*abort && t == 0) drain_ring(full, S, issued % S, uint32_t(issued / S) & 1, issued);
   if (!p.part) return;
   float* out = p.part + int64_t(blockIdx.x) * 2 * p.D;
   if (rpb == 1) {
