@@ -162,6 +162,12 @@ struct BwdParams {
   bool rms;
 };
 
+// A row of one or two elements has next to no gradient: gw, its mean and its
+// projection cancel down to their last bits (eps rstd^2 of gw remains).  This
+// kernel, which takes such rows, therefore rounds each product and sum of the
+// formula by itself; a fused multiply-add would leave another remainder than
+// the formula's terms do.
+//
 // NV groups per thread and row, R rows in flight per thread.
 template <bool BF16, int NV, int R, RowLayout L, bool DROP>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
@@ -219,7 +225,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
           aw[i][j] = fmaf(dy, xh, aw[i][j]);
           ab[i][j] += dy;
           c[2 * r] += gw;
-          c[2 * r + 1] = fmaf(gw, xh, c[2 * r + 1]);
+          c[2 * r + 1] = __fadd_rn(c[2 * r + 1], __fmul_rn(gw, xh));
         }
     }
     row_sum(c, p.tpr, red[buf]);
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
           const float dy = dyr[r][i].get(j);
           const float xh = (sr[r][i].get(j) - mu[r]) * rs[r];
           const float gw = dy * w.get(j);
-          d[j] = (gw - c1 - xh * c2) * rs[r];
+          d[j] = __fsub_rn(__fsub_rn(gw, __fmul_rn(xh, c2)), c1) * rs[r];
         }
         if (p.dsum_in) {
           const Raw8<BF16> a = load_raw8<BF16, L>(p.dsum_in, row * p.D, e);
