@@ -10,7 +10,7 @@
 // the two scales and rounds to the output type: three roundings of fp32 and
 // one of storage.
 //
-// Two kernels:
+// Three kernels:
 //  * tiles: many tokens.  Tokens take the MMA's M side; a pair of SMs shares a
 //    256 x 256 tile (cta_group::2), each holding half of either operand, so
 //    that an operand byte is fetched from L2 and read from shared memory once
@@ -22,6 +22,7 @@
 //    bound by HBM.  Where k is split too, the blocks of a cluster add their
 //    integer sums through distributed shared memory: no partial sums in
 //    memory, no counters, and integer adds give the same result in any order.
+//  * dots: a single token, on the CUDA cores; bound by HBM and by launching.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -642,6 +643,85 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// ---------------------------------------------------------------- dots
+
+// One token: each warp streams two channels' weights straight into registers,
+// 16 bytes per lane, against the token's bytes (which the L1 keeps), with the
+// four-way integer dot product of the CUDA cores.  Nothing is set up: no tensor
+// maps, barriers or tensor memory, whose 1.5 us before the first load the split
+// kernel has no work to hide behind here.  ksplit warps of a block share a pair
+// of channels where there are too few channels to keep HBM busy.  In a captured
+// run, against the split kernel: 8192 x 2048 5.8 us (6.8), 2048 x 8192 5.9
+// (8.4), 11008 x 4096 10.7 (12.0), 100352 x 2048 37.6 (38.2).  With two tokens
+// the two are even, with four the split kernel wins.
+constexpr int kDotThreads = 256, kDotWarps = kDotThreads / 32, kDotRows = 2;
+constexpr int kDotChunks = 4;              // chunks of 512 bytes in flight per row
+
+// 16 bytes of weights, read once; the loads stay in this order, ahead of what
+// uses them.
+__device__ __forceinline__ int4 load_weights(const int8_t* p, bool ok) {
+  int4 v = make_int4(0, 0, 0, 0);
+  if (ok)
+    asm volatile("ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+  return v;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kDotThreads)
+    dot_kernel(const int8_t* a, const int8_t* b, const Params p, int ksplit) {
+  __shared__ int part[kDotWarps][kDotRows];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kw = warp % ksplit;
+  const int n0 = (int(blockIdx.x) * (kDotWarps / ksplit) + warp / ksplit) * kDotRows;
+  wait_prior_kernels();
+  if (p.release) release_dependents();
+  int acc[kDotRows] = {};
+  const int8_t* row[kDotRows];
+#pragma unroll
+  for (int r = 0; r < kDotRows; ++r) row[r] = b + int64_t(min(n0 + r, p.N - 1)) * p.K;
+  // warp kw of a pair of channels takes every ksplit-th run of chunks
+  constexpr int kRun = kDotChunks * 512;
+  for (int k0 = kw * kRun + lane * 16; k0 < p.K; k0 += ksplit * kRun) {
+    int4 w[kDotChunks][kDotRows];
+#pragma unroll
+    for (int u = 0; u < kDotChunks; ++u)
+#pragma unroll
+      for (int r = 0; r < kDotRows; ++r)
+        w[u][r] = load_weights(row[r] + k0 + u * 512, k0 + u * 512 < p.K);
+#pragma unroll
+    for (int u = 0; u < kDotChunks; ++u) {
+      const int k = k0 + u * 512;
+      const int4 x = k < p.K ? *reinterpret_cast<const int4*>(a + k) : make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < kDotRows; ++r) {
+        acc[r] = __dp4a(w[u][r].x, x.x, acc[r]);
+        acc[r] = __dp4a(w[u][r].y, x.y, acc[r]);
+        acc[r] = __dp4a(w[u][r].z, x.z, acc[r]);
+        acc[r] = __dp4a(w[u][r].w, x.w, acc[r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kDotRows; ++r) {
+    const int s = __reduce_add_sync(0xffffffffu, acc[r]);
+    if (lane == 0) part[warp][r] = s;
+  }
+  if (ksplit > 1) __syncthreads();
+  else __syncwarp();
+  const int n = n0 + lane;
+  if (kw == 0 && lane < kDotRows && n < p.N) {
+    int s = 0;
+    for (int k = 0; k < ksplit; ++k) s += part[warp + k][lane];
+    const float v = float(s) * p.a_scale[0] * p.b_scale[n];
+    if constexpr (BF16)
+      static_cast<uint16_t*>(p.y)[n] = uint16_t(pack_bf2(v, 0.0f) & 0xffffu);
+    else
+      static_cast<float*>(p.y)[n] = v;
+  }
+}
+
 inline int cdiv(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 
 }  // namespace i8
@@ -751,6 +831,23 @@ staple_status go_split_c(const DeviceInfo& di, const CUtensorMap& w, const CUten
   }
 }
 
+template <bool BF16>
+staple_status go_dot(const DeviceInfo& di, const int8_t* a, const int8_t* b, const i8::Params& p,
+                     cudaStream_t st) {
+  // warps enough that their loads (128 bytes per lane) cover HBM's latency
+  const int pairs = i8::cdiv(p.N, i8::kDotRows);
+  int ksplit = 1;
+  while (ksplit < i8::kDotWarps && int64_t(pairs) * ksplit < int64_t(di.num_sms) * 16 &&
+         ksplit * i8::kDotChunks * 512 < p.K)
+    ksplit *= 2;
+  cudaError_t ce = cudaSuccess;
+  STP_LAUNCH("matmul_i8_dot", st,
+             ce = launch_dependent(i8::dot_kernel<BF16>,
+                                   dim3(unsigned(i8::cdiv(pairs, i8::kDotWarps / ksplit))),
+                                   i8::kDotThreads, 0, st, 1, a, b, p, ksplit));
+  return ce == cudaSuccess ? STAPLE_OK : STAPLE_ECUDA;
+}
+
 }  // namespace
 
 staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, int K,
@@ -772,6 +869,8 @@ staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, in
   p.err = err;
   p.wait_ns = di.wait_ns;
   p.release = release;
+  if (T == 1)
+    return bf16 ? go_dot<true>(di, a, b, p, st) : go_dot<false>(di, a, b, p, st);
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   CUtensorMap ma, mb, mo;

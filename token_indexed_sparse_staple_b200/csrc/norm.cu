@@ -62,6 +62,15 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
       if (p.res) rr[i] = load_raw8<BF16, L>(p.res, base, e);
     }
   }
+  // With few rows the weight and bias come from memory like the row itself:
+  // load them with it, not after its sums.
+  constexpr bool EARLY = NV == 1;
+  Raw8<BF16> w0 = ones_raw8<BF16>(), b0 = zero_raw8<BF16>();
+  if (EARLY) {
+    const Span e = span<L>(0, t, p.tpr, p.D);
+    if (p.w && e.n > 0) w0 = load_raw8<BF16, L>(p.w, 0, e);
+    if (p.b && e.n > 0) b0 = load_raw8<BF16, L>(p.b, 0, e);
+  }
   F2 v[NV][4];
   F2 s1 = f2(0.0f);
   DropKey key{};
@@ -136,9 +145,9 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
     const Span e = span<L>(i, t, p.tpr, p.D);
     if (e.n <= 0) break;
     // (a missing weight is ones, a missing bias is zeros)
-    Raw8<BF16> w = ones_raw8<BF16>(), b = zero_raw8<BF16>();
-    if (p.w) w = load_raw8<BF16, L>(p.w, 0, e);
-    if (p.b) b = load_raw8<BF16, L>(p.b, 0, e);
+    Raw8<BF16> w = w0, b = b0;
+    if (!EARLY && p.w) w = load_raw8<BF16, L>(p.w, 0, e);
+    if (!EARLY && p.b) b = load_raw8<BF16, L>(p.b, 0, e);
     float o[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
