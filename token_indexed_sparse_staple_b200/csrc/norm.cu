@@ -184,7 +184,8 @@ struct BwdParams {
 //
 // NV groups per thread and row, R rows in flight per thread.
 template <bool BF16, int NV, int R, RowLayout L, bool DROP>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(512, NV == 1 && R == 1 ? 2 : 1)
+    norm_bwd_kernel(const BwdParams p) {
   __shared__ float red[2][2 * R * 32];
   extern __shared__ float s_acc[];   // row groups' dw, db (several row groups per block)
   const int rpb = blockDim.x / p.tpr;
@@ -332,10 +333,9 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p) {
 // instructions per element, 17 of them dropout's).  The plain kernel above took
 // 117 us.
 //
-// NV groups of eight per thread and row, read from shared memory in both
-// passes.  Four of them make the two sums (10 shuffles and a barrier per row)
-// cheap against 32 elements and leave 128 registers enough for the 64 partial
-// sums of dw and db.
+// NV groups of eight per thread and row.  With two, what both passes use (gw
+// and xhat) stays in registers beside the 32 partial sums of dw and db; with
+// four (rows beyond 8192 elements) it is read and formed again.
 struct RingParams {
   BwdParams b;
   int32_t stages, tensors;   // tensors: 2, or 3 with dsum_in
@@ -588,9 +588,9 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
 }
 
 // dw[d], db[d] = sums over the blocks of the backward kernel, in block order
-// within each of 16 slices, then over the slices in order.  Block: 32 columns
-// x 16 slices.
-constexpr int kWgCols = 32, kWgSlices = 16;
+// within each of 32 slices, then over the slices in order.  Block: 32 columns
+// x 32 slices.
+constexpr int kWgCols = 32, kWgSlices = 32;
 __global__ void __launch_bounds__(kWgCols* kWgSlices)
     norm_wgrad_kernel(const float* part, int blocks, int D, float* dw, float* db) {
   __shared__ float s[kWgSlices][kWgCols];
@@ -865,8 +865,8 @@ staple_status launch_norm_bwd(const DeviceInfo& di, bool bf16, bool rms, int T, 
     p.tpr = threads_per_row(G, nv);
     const int rpb = std::max(1, 256 / p.tpr);
     const int block = rpb * p.tpr;
-    const int blocks = di.num_sms * std::max(1, 768 / block);
-    const int R = T <= int64_t(blocks) * rpb ? 1 : rows_in_flight(bf16, nv);
+    const int blocks = di.num_sms * std::max(1, 1024 / block);
+    const int R = T <= 4 * int64_t(blocks) * rpb ? 1 : rows_in_flight(bf16, nv);
     grid = std::min(std::min(cdiv(T, int64_t(rpb) * R), kNormMaxBlocks), blocks);
     const size_t smem = rpb > 1 ? size_t(rpb) * 2 * p.tpr * nv * kGroup * sizeof(float) : 0;
     r = bf16 ? bwd_nv<true>(p, nv, R, vec, grid, block, smem, st)
