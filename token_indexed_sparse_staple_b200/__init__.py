@@ -52,12 +52,20 @@ def _p(x) -> int | None:
         return x.ctypes.data if isinstance(x, np.ndarray) else int(x)
 
 
+def _current_stream() -> int:
+    """torch's current stream as a handle.  (torch.cuda.current_stream() builds
+    a Stream object, 3 us a call; these two lookups take 0.2.)"""
+    global _current_stream
+    import torch
+    torch.cuda.init()
+    device, handle = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _current_stream = lambda: handle(device())
+    return _current_stream()
+
+
 def _stream(s) -> int | None:
     if s is None:
-        # torch's current stream as a handle (torch.cuda.current_stream() builds
-        # a Stream object, 3 us a call)
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
