@@ -86,8 +86,9 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
     float e[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) e[j] = xr[i].get(j);
-    if (DROP) 
-      drop8(philox(key, uint64_t(row) * uint64_t(G) + (t + i * p.tpr)), p.drop.below, p.drop.scale, e);
+    if (DROP)
+      drop8(philox(key, uint64_t(row) * uint64_t(G) + (t + i * p.tpr)), p.drop.below,
+            p.drop.scale, e);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[i][j] = f2(e[2 * j], e[2 * j + 1]);
     if (p.sum) {
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(512, NV == 1 && R == 1 ? 2 : 1)
         if (p.dsum) store_raw8<BF16, L>(p.dsum, row * p.D, e, pack_raw8<BF16>(d));
         if (p.dx) {
           // from the fp32 gradient, not from the rounded dsum
-          if (DROP) 
+          if (DROP)
             drop8(philox(key, uint64_t(row) * uint64_t(G) + (t + i * p.tpr)), p.drop.below,
                   p.drop.scale, d);
           store_raw8<BF16, L>(p.dx, row * p.D, e, pack_raw8<BF16>(d));
