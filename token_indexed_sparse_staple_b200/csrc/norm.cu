@@ -43,7 +43,7 @@ struct FwdParams {
 
 // Forward.  One read of x and the residual, one write of the sum and y; a block
 // holds whole rows.  16384 x 2048 bf16 with residual takes 44.4 us without
-// dropout (6.05 TB/s, 0.94 of a copy) and 49.2 with it (0.85: the generator's
+// dropout (6.05 TB/s, 0.94 of a copy) and 47.5 with it (0.88: the generator's
 // integer products share the issue slots), 1 x 4096 takes 3.6 us, 1537 x 1023
 // fp32 7.7 (captured runs).
 template <bool BF16, int NV, RowLayout L, bool DROP>
@@ -78,6 +78,8 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
   }
   F2 v[NV][4];
   F2 s1 = f2(0.0f);
+  constexpr int B = NV < 2 ? 1 : 2;      // (more at a time would not fit the registers)
+  uint4 u[B];
   DropKey key{};
   if (DROP) key = drop_key(p.drop);
 #pragma unroll
@@ -86,9 +88,9 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
     float e[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) e[j] = xr[i].get(j);
-    if (DROP)
-      drop8(philox(key, uint64_t(row) * uint64_t(G) + (t + i * p.tpr)), p.drop.below,
-            p.drop.scale, e);
+    if (DROP && i % B == 0)
+      philox_n<B>(key, uint64_t(row) * uint64_t(G) + (t + i * p.tpr), uint32_t(p.tpr), u);
+    if (DROP) drop8(u[i % B], p.drop.below, p.drop.scale, e);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[i][j] = f2(e[2 * j], e[2 * j + 1]);
     if (p.sum) {
@@ -497,12 +499,8 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const RingParams rp)
     // row S - 1 steps ahead of this one
     if (t == 0 && row != row0 && row + (S - 1) * step < p.T && !*abort)
       fill(row + (S - 1) * step, st == 0 ? S - 1 : st - 1);
-    // the row's draws, generated side by side: one chain of ten rounds after
-    // the other would leave the warp waiting for its own results
     uint4 u[NV];
-    if (DROP)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) u[i] = philox(key, uint64_t(row) * uint64_t(G) + (t + i * p.tpr));
+    if (DROP) philox_n<NV>(key, uint64_t(row) * uint64_t(G) + t, uint32_t(p.tpr), u);
     const F2 nc1 = f2(p.rms ? 0.0f : -a0 * inv_d), nc2 = f2(-b0 * inv_d);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

@@ -222,6 +222,31 @@ __device__ __forceinline__ uint4 philox(const DropKey& k, uint64_t n) {
   return make_uint4(c0, c1, c2, c3);
 }
 
+// The draws of N groups n0, n0 + step, ..., round by round: the key's schedule
+// is then worked out once for all of them, and no chain of ten rounds leaves
+// the warp waiting for its own results.
+template <int N>
+__device__ __forceinline__ void philox_n(const DropKey& k, uint64_t n0, uint32_t step,
+                                         uint4 (&u)[N]) {
+  uint32_t k0 = k.k0, k1 = k.k1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint64_t n = n0 + uint64_t(i) * step;
+    u[i] = make_uint4(uint32_t(n), uint32_t(n >> 32), k.c2, k.c3);
+  }
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint64_t p0 = uint64_t(u[i].x) * 0xD2511F53u, p1 = uint64_t(u[i].z) * 0xCD9E8D57u;
+      u[i] = make_uint4(uint32_t(p1 >> 32) ^ u[i].y ^ k0, uint32_t(p1),
+                        uint32_t(p0 >> 32) ^ u[i].w ^ k1, uint32_t(p0));
+    }
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+
 // v[i] = kept ? v[i] * scale : 0 for eight elements with the draws u.  A dropped
 // element is zero whatever it held (an infinity or a NaN included).  A draw in
 // the high half is compared without taking it out of its word; thr = 2^16
