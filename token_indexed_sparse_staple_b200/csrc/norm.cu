@@ -663,12 +663,14 @@ constexpr int rows_in_flight(bool bf16, int nv) {
 template <bool BF16, int NV, int R>
 staple_status bwd_go(const BwdParams& p, bool vec, int grid, int block, size_t smem,
                      cudaStream_t st) {
-  void (*kern)(BwdParams);
-  if (p.drop.rng)
-    kern = vec ? norm_bwd_kernel<BF16, NV, R, VEC, true> : norm_bwd_kernel<BF16, NV, R, GROUP, true>;
-  else
-    kern = vec ? norm_bwd_kernel<BF16, NV, R, VEC, false>
-               : norm_bwd_kernel<BF16, NV, R, STRIDE, false>;
+  void (*kern)(BwdParams) = p.drop.rng ? norm_bwd_kernel<BF16, NV, R, GROUP, true>
+                                       : norm_bwd_kernel<BF16, NV, R, STRIDE, false>;
+  // whole vectors come here only from rows too short for the ring kernel, and
+  // from fp32 rows too long for it
+  if constexpr (NV == 1 || (NV == 4 && !BF16))
+    if (vec)
+      kern = p.drop.rng ? norm_bwd_kernel<BF16, NV, R, VEC, true>
+                        : norm_bwd_kernel<BF16, NV, R, VEC, false>;
   cudaError_t ce = cudaSuccess;
   STP_LAUNCH("norm_bwd", st,
              ce = launch_dependent(kern, dim3(unsigned(grid)), unsigned(block), smem, st, 1, p));
@@ -697,8 +699,7 @@ struct RingPlan {
 bool plan_ring(int D, int es, int tensors, RingPlan* out) {
   const int G = D / kGroup;
   RingPlan r{};
-  // fp32 groups are twice as wide: four per thread would not leave the
-  // partial sums their registers (only rows beyond 8192 need them)
+  // (four only where two would need more than 512 threads)
   r.nv = G > 1024 ? 4 : (G > 32 ? 2 : 1);
   r.tpr = std::max(32, threads_per_row(G, r.nv));
   // one block of 512 threads per SM: fewer blocks leave fewer partial sums of
