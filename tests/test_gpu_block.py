@@ -169,6 +169,47 @@ def test_i8_layer_keeps_a_bad_row_to_itself(stp, ctx):
     assert torch.isnan(m.y[~rows]).all()
 
 
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("T,D,F", [(1, 256, 512), (1, 1024, 8192), (7, 1024, 2048)])
+def test_i8_layer_reads_weights_written_just_before_it(stp, ctx, T, D, F, graph):
+    """The layer's kernels start early and may load weights early; weights that the
+    work in front of the call writes on the same stream are still the ones read."""
+    import torch
+    a, b = (I8Layer(stp, ctx, T, D, F, 64, seed=s) for s in (1, 2))
+    e = a.embed("table")
+    names = ("w_gate_up", "gate_up_scale", "w_down", "down_scale")
+    want, saved = [], [{n: getattr(l.q, n).clone() for n in names} for l in (a, b)]
+    for s in saved:
+        for n in names:
+            getattr(a.q, n).copy_(s[n])
+        torch.cuda.synchronize()
+        a.run(e)
+        torch.cuda.synchronize()
+        want.append(a.y.clone())
+    assert not torch.equal(*want)
+    got = torch.full((8, T, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+
+    def alternate(stream):
+        for i in range(8):
+            for n in names:
+                getattr(a.q, n).copy_(saved[i % 2][n])
+            a.run(e, y=got[i], stream=stream)
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=st):
+                alternate(st)
+            g.replay()
+        else:
+            alternate(st)
+    torch.cuda.synchronize()
+    for i in range(8):
+        assert torch.equal(got[i], want[i % 2])
+
+
 @pytest.mark.parametrize("i8, norms", [(False, True), (True, False), (True, True)])
 def test_decode_stack_runs_the_same_operators(stp, ctx, i8, norms):
     """A captured step of the stack equals the same public calls made one by

@@ -169,10 +169,13 @@ staple_status launch_gate_quant(const DeviceInfo& di, int T, int F, const void* 
 // matmul_i8.cu: K is at most kI8MaxK, so that no sum of products of two 8-bit
 // numbers leaves 32 bits (2^14 K < 2^31)
 constexpr int kI8MaxK = (1 << 17) - 16;
+// release: the next kernel may start as soon as this one has itself waited for what
+// came before it. weights_ready: b may be read before the kernel in front has
+// completed, because that one does not write b and was launched with release
 staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, int K,
                                const int8_t* a, const float* a_scale, const int8_t* b,
                                const float* b_scale, void* y, int32_t* err, cudaStream_t st,
-                               bool release = false);
+                               bool release = false, bool weights_ready = false);
 
 // simt_f32.cu (fp32 on CUDA cores)
 staple_status f32_ffn_fwd(int T, int D, int F, const float* x, const staple_embed* e,

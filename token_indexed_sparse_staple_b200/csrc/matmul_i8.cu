@@ -139,6 +139,7 @@ struct Params {
   int32_t* err;
   uint64_t wait_ns;
   bool release;          // the next kernel is part of the same call
+  bool weights_ready;    // dot_kernel may read b before wait_prior_kernels()
   // tiles
   int32_t tiles_t, tiles_n, group_t;
   bool tma_out;
@@ -681,21 +682,25 @@ __global__ void __launch_bounds__(kDotThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kw = warp % ksplit;
   const int n0 = (int(blockIdx.x) * (kDotWarps / ksplit) + warp / ksplit) * kDotRows;
-  wait_prior_kernels();
-  if (p.release) release_dependents();
+  if (!p.weights_ready) wait_prior_kernels();
   int acc[kDotRows] = {};
   const int8_t* row[kDotRows];
 #pragma unroll
   for (int r = 0; r < kDotRows; ++r) row[r] = b + int64_t(min(n0 + r, p.N - 1)) * p.K;
   // warp kw of a pair of channels takes every ksplit-th run of chunks
   constexpr int kRun = kDotChunks * 512;
-  for (int k0 = kw * kRun + lane * 16; k0 < p.K; k0 += ksplit * kRun) {
+  for (int kr = kw * kRun; kr < p.K; kr += ksplit * kRun) {
+    const int k0 = kr + lane * 16;
     int4 w[kDotChunks][kDotRows];
 #pragma unroll
     for (int u = 0; u < kDotChunks; ++u)
 #pragma unroll
       for (int r = 0; r < kDotRows; ++r)
         w[u][r] = load_weights(row[r] + k0 + u * 512, k0 + u * 512 < p.K);
+    // the first weights are on their way while the kernel in front finishes: in the
+    // 8-bit layer of one token (2048 -> 8192 -> 2048) 19 -> 15 us. (In split_kernel
+    // the same made no difference above the noise of 2 us at 64 tokens: left out.)
+    if (p.weights_ready && kr == kw * kRun) wait_prior_kernels();
 #pragma unroll
     for (int u = 0; u < kDotChunks; ++u) {
       const int k = k0 + u * 512;
@@ -716,6 +721,8 @@ __global__ void __launch_bounds__(kDotThreads)
   }
   if (ksplit > 1) __syncthreads();
   else __syncwarp();
+  if (p.weights_ready) wait_prior_kernels();    // (a warp without a run has not waited yet)
+  if (p.release) release_dependents();
   const int n = n0 + lane;
   if (kw == 0 && lane < kDotRows && n < p.N) {
     int s = 0;
@@ -859,7 +866,7 @@ staple_status go_dot(const DeviceInfo& di, const int8_t* a, const int8_t* b, con
 staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, int K,
                                const int8_t* a, const float* a_scale, const int8_t* b,
                                const float* b_scale, void* y, int32_t* err, cudaStream_t st,
-                               bool release) {
+                               bool release, bool weights_ready) {
   if (T == 0) return STAPLE_OK;
   // tiles are counted in 32 bits
   if (int64_t(i8::cdiv(T, 2 * i8::BM)) * i8::cdiv(N, i8::BN) > INT32_MAX / 2)
@@ -875,6 +882,7 @@ staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, in
   p.err = err;
   p.wait_ns = di.wait_ns;
   p.release = release;
+  p.weights_ready = weights_ready;
   if (T == 1)
     return bf16 ? go_dot<true>(di, a, b, p, st) : go_dot<false>(di, a, b, p, st);
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;

@@ -897,10 +897,10 @@ staple_status staple_ffn_fwd_i8(staple_context* ctx, int32_t T, int32_t D, int32
   const bool up = !replaces_up(embed);
   STP_TRY(stp::launch_quant_rows(ctx->di, true, T, D, x, xq, xs, st, true));
   STP_TRY(stp::launch_matmul_i8(ctx->di, true, T, up ? 2 * F : F, D, xq, xs, w_gate_up,
-                                gate_up_scale, ws + l.gu, ctx->d_err, st, true));
+                                gate_up_scale, ws + l.gu, ctx->d_err, st, true, true));
   STP_TRY(stp::launch_gate_quant(ctx->di, T, F, ws + l.gu, up, embed, zq, zs, ctx->d_err, st));
   return stp::launch_matmul_i8(ctx->di, true, T, D, F, zq, zs, w_down, down_scale, y, ctx->d_err,
-                               st);
+                               st, false, true);
 }
 
 }  // extern "C"
