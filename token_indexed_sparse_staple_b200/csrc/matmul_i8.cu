@@ -139,7 +139,7 @@ struct Params {
   int32_t* err;
   uint64_t wait_ns;
   bool release;          // the next kernel is part of the same call
-  bool weights_ready;    // dot_kernel may read b before wait_prior_kernels()
+  bool weights_ready;    // b may be read before wait_prior_kernels() (split and dot)
   // tiles
   int32_t tiles_t, tiles_n, group_t;
   bool tma_out;
@@ -503,11 +503,17 @@ __global__ void __launch_bounds__(kThreads)
     }
     fence_barrier_init();
     if (lane < first) mbar_arrive_expect_tx(&full[lane], stage_bytes);
-    wait_prior_kernels();
     __syncwarp();
+    // In the 8-bit layer the first ring of weights is on its way while the kernel in
+    // front finishes: 64 x 4096 x 11008 37 us with it and the gate's early E, 40
+    // without; prefetching the weights behind the ring into L2 too gained nothing.
+    if (p.weights_ready && lane == 0)
+      for (int s = 0; s < first; ++s) load_w(s, s);
+    __syncwarp();
+    wait_prior_kernels();
     if (lane == 0)
       for (int s = 0; s < first; ++s) {
-        load_w(s, s);
+        if (!p.weights_ready) load_w(s, s);
         load_x(s, s);
       }
     __syncwarp();
@@ -698,8 +704,7 @@ __global__ void __launch_bounds__(kDotThreads)
       for (int r = 0; r < kDotRows; ++r)
         w[u][r] = load_weights(row[r] + k0 + u * 512, k0 + u * 512 < p.K);
     // the first weights are on their way while the kernel in front finishes: in the
-    // 8-bit layer of one token (2048 -> 8192 -> 2048) 19 -> 15 us. (In split_kernel
-    // the same made no difference above the noise of 2 us at 64 tokens: left out.)
+    // 8-bit layer of one token (2048 -> 8192 -> 2048) 19 -> 15 us
     if (p.weights_ready && kr == kw * kRun) wait_prior_kernels();
 #pragma unroll
     for (int u = 0; u < kDotChunks; ++u) {
@@ -744,7 +749,9 @@ struct SplitPlan {
   int cluster, rows, stages, smem;
 };
 
-constexpr int kSplitSmemMax = 225 * 1024;   // beside 1.5 KB of static arrays
+// Beside 1.5 KB of static arrays and the 1 KB that each block takes; a quantiser's
+// block (the kernel in front in the 8-bit layer) still fits in what is left of 228.
+constexpr int kSplitSmemMax = 223 * 1024;
 
 // Every candidate cluster size with the tile height that fills the SMs (w
 // blocks each), and the estimated time on one SM in us: its share of the
@@ -777,7 +784,7 @@ SplitPlan plan_split(int num_sms, int N, int units, int tokens, int tiles_t, int
     int stages = 0;
     for (int fit = std::min(w, 512 / cols > 1 ? 2 : 1); fit >= 1 && stages < std::min(3, per_block); --fit)
       stages = std::min(std::min(per_block, i8::kMaxStages),
-                        (std::min(228 * 1024 / fit - 3072, kSplitSmemMax) - 1024 - over) / stage);
+                        (std::min(228 * 1024 / fit - 4096, kSplitSmemMax) - 1024 - over) / stage);
     const int want = std::max(stages * stage + over, c > 1 ? tokens * i8::BM * 4 : 0) + 1024;
     // Blocks that share an SM share its 512 columns of tensor memory, and a
     // block that waits for columns could wait for a cluster whose other blocks

@@ -51,6 +51,21 @@ __device__ __forceinline__ uint32_t q_exact(float x, double scale) {
   return uint32_t(int(d)) & 0xffu;
 }
 
+// The same for a row of ordinary scale, without a division.  The candidate q is
+// off by one at most, and only where x lies within 2^-13 scales of a tie.  There
+// r = x - q scale is exact: x is at least half the scale's power of two 2^e, so x
+// and q scale are multiples of 2^(e-24), and |r| < 2^e.  (For a smaller x, whose
+// quotient is below 1/2, the nearest is 0; a candidate of 1 gives an |r| that
+// rounds to half the scale or more, and goes to 0 either way.)
+__device__ __forceinline__ uint32_t q_near(float x, float inv, float scale) {
+  const float m = fmaf(x, inv, kRintMagic);
+  float q = m - kRintMagic;
+  const float r = fmaf(-scale, q, x), half = 0.5f * scale;
+  const bool odd = __float_as_uint(m) & 1u;
+  if (fabsf(r) > half || (fabsf(r) == half && odd)) q += copysignf(1.0f, r);
+  return uint32_t(int(q)) & 0xffu;
+}
+
 // A group's eight bytes.
 template <RowLayout L>
 __device__ __forceinline__ void store8(int8_t* row, const Span& s, uint32_t lo, uint32_t hi) {
@@ -68,58 +83,65 @@ __device__ __forceinline__ float gated(float g, float u, float e) {
   return g * sigmoid_f(g) * (u + e);
 }
 
-// One element of a row, as the kernel below loads it.
-template <bool BF16, bool GATE>
-__device__ __forceinline__ float element(const QuantParams& p, int64_t row, int d,
-                                         const uint16_t* e_row) {
-  const uint16_t* h = static_cast<const uint16_t*>(p.x);
-  if constexpr (GATE) {
-    const uint16_t* g = h + row * p.pitch + d;
-    const float z = gated(bf2f(g[0]), p.up ? bf2f(g[p.up]) : 0.0f, e_row ? bf2f(e_row[d]) : 0.0f);
-    return bf_lo(pack_bf2(z, 0.0f));
-  } else {
-    return BF16 ? bf2f(h[row * p.D + d]) : static_cast<const float*>(p.x)[row * p.D + d];
-  }
-}
-
 // GATE: the row is not x but the layer's gated product z = SiLU(g) (u + E),
 // rounded to bf16 as the layer stores it, which thus never goes to memory.
 template <bool BF16, int NV, RowLayout L, bool GATE>
 // (bf16: 64 registers, so that 32 warps share an SM)
-__global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(GATE ? 1024 : 512, BF16 && !GATE ? 2 : 1)
+    quant_rows_kernel(const QuantParams p) {
   __shared__ uint32_t red[32];
   const int rpb = blockDim.x / p.tpr;
   const int rg = threadIdx.x / p.tpr, t = threadIdx.x - rg * p.tpr;
   const int64_t row = int64_t(blockIdx.x) * rpb + rg;
   const bool row_ok = row < p.T;
   const int64_t base = row * p.D;
-  wait_prior_kernels();
-  if (p.release) release_dependents();
+  if constexpr (!GATE) {
+    wait_prior_kernels();
+    if (p.release) release_dependents();
+  }
+  // E is there before the product in front has run: that one releases this kernel
+  // only after it has itself waited for all before it, and does not write E or the
+  // ids.
   const uint16_t* e_row = nullptr;
   if (GATE && row_ok && p.e_base) {
     const int64_t idx = p.e_index[row];
     if (idx < 0 || idx >= p.e_rows) report(p.err, STAPLE_EIDRANGE);
     else e_row = p.e_base + idx * p.e_pitch;
   }
+  // (eight groups per thread leave no registers to hold it)
+  constexpr bool kEarlyE = GATE && NV <= 4;
+  Raw8<true> early[kEarlyE ? NV : 1];
+  if constexpr (kEarlyE) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Span s = span<L>(i, t, p.tpr, p.D);
+      early[i] = e_row && s.n > 0 ? load_raw8<true, VEC>(e_row, 0, s) : zero_raw8<true>();
+    }
+  }
+  if constexpr (GATE) {
+    wait_prior_kernels();
+    if (p.release) release_dependents();
+  }
+  auto load_group = [&](const Span& s, int i) {
+    if constexpr (GATE) {
+      const Raw8<true> gr = load_raw8<true, VEC>(p.x, row * p.pitch, s);
+      Raw8<true> ur = zero_raw8<true>(), er = zero_raw8<true>();
+      if (p.up) ur = load_raw8<true, VEC>(p.x, row * p.pitch + p.up, s);
+      if constexpr (kEarlyE) er = early[i];
+      else if (e_row) er = load_raw8<true, VEC>(e_row, 0, s);
+      float z[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = gated(gr.get(j), ur.get(j), er.get(j));
+      return pack_raw8<true>(z);
+    } else {
+      return load_raw8<BF16, L>(p.x, base, s);
+    }
+  };
   Raw8<BF16> xr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const Span s = span<L>(i, t, p.tpr, p.D);
-    xr[i] = zero_raw8<BF16>();
-    if (row_ok && s.n > 0) {
-      if constexpr (GATE) {
-        const Raw8<true> gr = load_raw8<true, VEC>(p.x, row * p.pitch, s);
-        Raw8<true> ur = zero_raw8<true>(), er = zero_raw8<true>();
-        if (p.up) ur = load_raw8<true, VEC>(p.x, row * p.pitch + p.up, s);
-        if (e_row) er = load_raw8<true, VEC>(e_row, 0, s);
-        float z[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = gated(gr.get(j), ur.get(j), er.get(j));
-        xr[i] = pack_raw8<true>(z);
-      } else {
-        xr[i] = load_raw8<BF16, L>(p.x, base, s);
-      }
-    }
+    xr[i] = row_ok && s.n > 0 ? load_group(s, i) : zero_raw8<BF16>();
   }
   // the largest |x| as bits: a NaN is above the infinity, which is above
   // every finite number
@@ -155,7 +177,8 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
   const bool finite = m < 0x7f800000u;
   if (t == 0) p.scale[row] = scale;
   // (an approximate reciprocal will do: the remainder decides)
-  const F2 inv = f2(__fdividef(1.0f, scale)), nscale = f2(-scale);
+  const float inv1 = __fdividef(1.0f, scale);
+  const F2 inv = f2(inv1), nscale = f2(-scale);
   const F2 magic = f2(kRintMagic), nmagic = f2(-kRintMagic);
   const bool fast = finite && amax >= kTiny;
   const float half = fast ? 0.5f * scale : 0.0f;
@@ -185,20 +208,45 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) quant_rows_kernel(const Qua
     store8<L>(p.q + base, s, lo, hi);
     if (!(worst < half)) redo |= 1u << i;
   }
-  // groups that need the division (and all of a row that is tiny, zero or not
+  // groups with an element at a tie (and all of a row that is tiny, zero or not
   // finite), behind the others so that no branch stands between their loads
-  // and stores; their elements are read again
+  // and stores; one at a time
   while (redo) {
     const int i = __ffs(int(redo)) - 1;
     redo &= redo - 1;
     const Span s = span<L>(i, t, p.tpr, p.D);
+    Raw8<BF16> x = xr[0];
+    if constexpr (NV == 8) {     // (read again: fewer registers)
+      x = load_group(s, 0);
+    } else {
+#pragma unroll
+      for (int k = 1; k < NV; ++k)
+        if (k == i) x = xr[k];
+    }
     uint32_t lo = 0, hi = 0;
+    if (fast) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        lo |= q_near(x.get(j), inv1, scale) << (8 * j);
+        hi |= q_near(x.get(j + 4), inv1, scale) << (8 * j);
+      }
+      store8<L>(p.q + base, s, lo, hi);
+      continue;
+    }
 #pragma unroll 1
-    for (int j = 0; j < s.n; ++j) {
-      const float x = element<BF16, GATE>(p, row, s.off + j * s.step, e_row);
-      const uint32_t v = finite && scale > 0.0f ? q_exact(x, double(scale)) : 0u;
-      if (j < 4) lo |= v << (8 * j);
-      else hi |= v << (8 * j - 32);
+    for (int j = 0; j < kGroup; ++j) {
+      const uint32_t v = finite && scale > 0.0f ? q_exact(x.get(0), double(scale)) : 0u;
+      // the bytes enter at the top, the elements leave at the bottom
+      lo = __funnelshift_r(lo, hi, 8);
+      hi = hi >> 8 | v << 24;
+      if constexpr (BF16) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) x.w[k] = __funnelshift_r(x.w[k], x.w[k + 1], 16);
+        x.w[3] >>= 16;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 7; ++k) x.w[k] = x.w[k + 1];
+      }
     }
     store8<L>(p.q + base, s, lo, hi);
   }
@@ -211,7 +259,10 @@ cudaError_t go(const DeviceInfo& di, QuantParams p, cudaStream_t st) {
   // is found with few instructions per element (16384 x 8192 bf16: 125 us with
   // two, 80 with four, 73 with eight)
   const int G = groups_of(p.D);
-  const int few = G > 2048 ? 8 : (G > 1024 ? 4 : (G > 512 ? 2 : 1));
+  // (GATE's three loads per group want more threads: 64 x 4096 x 11008 as a
+  // layer takes 35.7 us with 704 per row, 37.0 with 352)
+  const int per = G / (GATE ? 2 : 1);
+  const int few = per > 2048 ? 8 : (per > 1024 ? 4 : (G > 512 ? 2 : 1));
   const int many = G > 128 ? 8 : (G > 64 ? 4 : (G > 32 ? 2 : 1));
   const int nv = p.T <= 2 * di.num_sms ? few : many;
   p.tpr = threads_per_row(G, nv);
