@@ -79,6 +79,25 @@ def test_matches_the_definition(stp, ctx, T, N, K, dtype):
     assert stp.staple_get_error(ctx) == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T, N, K", [(129, 16384, 512), (200, 22016, 1040), (256, 12345, 528),
+                                     (600, 9600, 2048), (1000, 2052, 784), (130, 600, 4112),
+                                     (600, 200, 4096), (1100, 515, 8192)])
+def test_either_kernel_above_half_a_tile_of_tokens(stp, ctx, T, N, K, dtype):
+    """Both sides of the choice between the tiles and the split kernel, with rows,
+    channels and k that no tile divides, at an output address of the element's size."""
+    import torch
+    ops = operands(T, N, K, T + K, full_range=True)
+    check(run(stp, ctx, dtype, *ops), *ops, dtype)
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    buf = torch.full((T * N + 2,), 7.0, dtype=td, device="cuda")
+    y = buf[1:1 + T * N].view(T, N)
+    run(stp, ctx, dtype, *ops, y=y)
+    check(y, *ops, dtype)
+    assert buf[0] == 7 and buf[-1] == 7
+    assert stp.staple_get_error(ctx) == 0
+
+
 def test_against_the_numpy_definition(stp, ctx):
     for dtype in ("bf16", "f32"):
         a, sa, b, sb = operands(19, 37, 80, 3)

@@ -746,6 +746,7 @@ inline int cdiv(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 // How a few-tiles product is cut.
 struct SplitPlan {
   int cluster, rows, stages, smem;
+  double us;           // of the whole launch, estimated; see tiles_us
 };
 
 // Beside 1.5 KB of static arrays and the 1 KB that each block takes; a quantiser's
@@ -796,9 +797,24 @@ SplitPlan plan_split(int num_sms, int N, int units, int tokens, int tiles_t, int
     const int share = std::max(int(int64_t(cols) * 228 * 1024 / 512) - 1024,
                                (c > 1 ? 84 : 36) * 1024);
     best_us = us;
-    best = SplitPlan{c, rows, stages, std::max(want, share)};
+    const double total = 4.0 +
+                         w * per_block * std::max(0.3, (rows + 0.15 * tokens) * i8::kUnit / 43600.0) +
+                         (c == 1 ? 0.025 : 0.02) * tokens * w;
+    best = SplitPlan{c, rows, stages, std::max(want, share), total};
   }
   return best;
+}
+
+// The time of the pair's tiles, to choose between the two kernels above half a
+// tile's 256 tokens (below, the split kernel wins): a start and an end, and per
+// round of tiles its k and its epilogue.  This and the split estimate (a start and
+// an end, the units, the tokens' epilogue) were fitted to captured runs of 110
+// shapes (160 to 4096 tokens, N 512 to 28672, K 64 to 28672) and pick the faster
+// or one within 5 % each time.  Split against tiles: 192 x 8192 x 2048 11.7 / 12.4
+// us, 192 x 16384 x 2048 15.2 / 13.6, 256 x 22016 x 4096 48.4 / 28.2, 256 x 4096 x
+// 11008 19.8 / 31.3, 512 x 8192 x 2048 17.6 / 13.0, 1024 x 2048 x 8192 22.7 / 25.4.
+double tiles_us(int pairs, int64_t tiles, int K) {
+  return 7.0 + (0.3 * i8::cdiv(K, i8::BK) + 0.5) * i8::cdiv(tiles, pairs);
 }
 
 template <typename K>
@@ -811,6 +827,8 @@ bool opt_in(K kern, int bytes, int device, std::atomic<uint64_t>& done) {
   return true;
 }
 
+int tile_pairs(const DeviceInfo& di) { return std::max(1, (di.num_sms - di.sm_reserve) / 2); }
+
 template <bool BF16>
 staple_status go_tiles(const DeviceInfo& di, const CUtensorMap& a, const CUtensorMap& b,
                        const CUtensorMap& o, const i8::Params& p, cudaStream_t st) {
@@ -818,8 +836,7 @@ staple_status go_tiles(const DeviceInfo& di, const CUtensorMap& a, const CUtenso
   auto kern = i8::tiles_kernel<BF16>;
   if (!opt_in(kern, i8::kTilesSmem, di.device, done)) return STAPLE_ECUDA;
   const int ntiles = p.tiles_t * p.tiles_n;
-  const int pairs = std::max(1, (di.num_sms - di.sm_reserve) / 2);
-  const int per = i8::cdiv(ntiles, pairs);
+  const int per = i8::cdiv(ntiles, tile_pairs(di));
   cudaError_t ce = cudaSuccess;
   STP_LAUNCH("matmul_i8", st,
              ce = launch_dependent(kern, dim3(2 * unsigned(i8::cdiv(ntiles, per))), i8::kThreads,
@@ -897,7 +914,21 @@ staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, in
   CUtensorMap ma, mb, mo;
   p.tiles_t = i8::cdiv(T, 2 * i8::BM);
   p.tiles_n = i8::cdiv(N, i8::BN);
-  if (T > i8::kMaxTokens && int64_t(p.tiles_t) * p.tiles_n >= di.num_sms / 2) {
+  const int tiles_t = i8::cdiv(T, i8::kMaxTokens);
+  p.tokens = std::min(i8::kMaxTokens, i8::cdiv(T, 16) * 16);
+  p.cols = 32;
+  while (p.cols < p.tokens) p.cols <<= 1;
+  p.units = i8::cdiv(K, i8::kUnit);
+  const int64_t tiles = int64_t(p.tiles_t) * p.tiles_n;
+  const int pairs = tile_pairs(di);
+  // (with many tiles there is nothing to weigh)
+  SplitPlan pl{};
+  bool by_tiles = T > i8::BM && tiles > 4 * int64_t(pairs);
+  if (!by_tiles) {
+    pl = plan_split(di.num_sms, N, p.units, p.tokens, tiles_t, p.cols);
+    by_tiles = T > i8::BM && tiles_us(pairs, tiles, K) < pl.us;
+  }
+  if (by_tiles) {
     p.group_t = 8;
     p.tma_out = (int64_t(N) * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
     if (!tensor_map_2d(&ma, u8, 1, a, K, T, K, i8::BK, i8::BM, sw) ||
@@ -911,13 +942,7 @@ staple_status launch_matmul_i8(const DeviceInfo& di, bool bf16, int T, int N, in
       return STAPLE_ECUDA;
     return bf16 ? go_tiles<true>(di, ma, mb, mo, p, st) : go_tiles<false>(di, ma, mb, mo, p, st);
   }
-  const int tiles_t = i8::cdiv(T, i8::kMaxTokens);
-  p.tokens = std::min(i8::kMaxTokens, i8::cdiv(T, 16) * 16);
-  p.cols = 32;
-  while (p.cols < p.tokens) p.cols <<= 1;
-  p.units = i8::cdiv(K, i8::kUnit);
   p.vec_out = (N % 4) == 0 && (reinterpret_cast<uintptr_t>(y) & uintptr_t(4 * es - 1)) == 0;
-  const SplitPlan pl = plan_split(di.num_sms, N, p.units, p.tokens, tiles_t, p.cols);
   p.rows = pl.rows;
   p.stages = pl.stages;
   if (!tensor_map_2d(&mb, u8, 1, b, K, N, K, i8::BK, uint32_t(p.rows), sw) ||
