@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the tiles are as many as the SMs.  Only outputs too narrow for that, or with
 // so many tokens that their re-reading from L2 would cost more, split k too.
 // 64 x 11008 x 4096 takes 11.0 us a call among others (45 MB of weights in 6.5
-// of them), 64 x 8192 x 2048 7.7 in a captured run.
+// of them), 64 x 8192 x 2048 7.9 in a captured run.
 constexpr int kUnit = 2 * BK;               // 256 bytes of each row per stage
 constexpr int kMaxTokens = 256, kMaxStages = 24;
 
@@ -663,9 +663,9 @@ __global__ void __launch_bounds__(kThreads)
 // maps, barriers or tensor memory, whose 1.5 us before the first load the split
 // kernel has no work to hide behind here.  ksplit warps of a block share a pair
 // of channels where there are too few channels to keep HBM busy.  In a captured
-// run, against the split kernel: 8192 x 2048 5.8 us (6.8), 2048 x 8192 5.9
-// (8.4), 11008 x 4096 10.7 (12.0), 100352 x 2048 37.6 (38.2).  With two tokens
-// the two are even, with four the split kernel wins.
+// run, beside two tokens in the split kernel: 8192 x 2048 4.8 us (6.7), 2048 x
+// 8192 4.5 (7.6), 11008 x 4096 9.3 (11.1).  Given two tokens the two kernels were
+// even, given four the split kernel won.
 constexpr int kDotThreads = 256, kDotWarps = kDotThreads / 32, kDotRows = 2;
 constexpr int kDotChunks = 4;              // chunks of 512 bytes in flight per row
 
@@ -758,11 +758,12 @@ constexpr int kSplitSmemMax = 223 * 1024;
 // weights at its share of HBM (43.6 KB per us) with the tokens' rows once more
 // per tile at about 2.5 times that from L2, at least 0.3 per unit to issue its
 // products, 1 for each further block per SM, and the sum over a cluster.
-// Measured in a captured run: 64 x 4096 x 11008 takes 14.1 us in clusters of
-// 4 (128 rows) against 19.2 without (32 rows); 64 x 11008 x 4096 takes 12.8
-// without (80 rows) against 14.3 in pairs; 256 x 8192 x 2048 takes 15.5 in
-// pairs against 16.7 without.  Clusters do not pack all SMs (33 of 4 and 15 of
-// 8 fit at one block per SM).
+// Measured in a captured run: 64 x 4096 x 11008 takes 12.3 us in clusters of
+// 4 (128 rows) against 17.7 without (32 rows); 64 x 11008 x 4096 takes 12.0
+// without (80 rows) against 13.2 in pairs; 128 x 8192 x 8192 takes 17.7 in
+// pairs against 20.1 without.  Over 65 shapes of 2 to 256 tokens the choice was
+// the best or 1 % behind it on average, 13 % at most.  Clusters do not pack all
+// SMs (33 of 4 and 15 of 8 fit at one block per SM).
 SplitPlan plan_split(int num_sms, int N, int units, int tokens, int tiles_t, int cols) {
   SplitPlan best{};
   double best_us = 1e30;
