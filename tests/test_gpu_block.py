@@ -276,6 +276,66 @@ def test_decode_stack_runs_the_same_operators(stp, ctx, i8, norms):
         tables.close()
 
 
+def test_layers_side_by_side_on_streams_of_their_own(stp, ctx):
+    """8-bit layers of one token, of clusters and of tiles beside the bf16 decode
+    kernel and a norm's backward pass: each gives what it gives alone."""
+    import torch
+    layers = [I8Layer(stp, ctx, T, D, F, 64, seed=T) for T, D, F in
+              ((1, 1024, 4096), (64, 2048, 8192), (64, 1024, 12288), (200, 1024, 8192))]
+    embeds = [m.embed("table") for m in layers]
+    m = layers[1]
+    T, D, F = m.T, m.D, m.F
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    wg, wu, wd = ((torch.randn(s, generator=g, device="cuda") * 0.02).to(torch.bfloat16)
+                  for s in ((F, D), (F, D), (D, F)))
+    z = torch.empty((T, F), dtype=torch.bfloat16, device="cuda")
+    wsb = stp.staple_workspace_bytes(T, D, F)
+    ws = torch.zeros(wsb, dtype=torch.uint8, device="cuda")
+    rows = 4000
+    dy, s_in = ((torch.randn((rows, D), generator=g, device="cuda")).to(torch.bfloat16)
+                for _ in range(2))
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    y0 = torch.empty_like(s_in)
+    mean, rstd = (torch.empty(rows, device="cuda") for _ in range(2))
+    stp.staple_norm_fwd(ctx, stp.STAPLE_BF16, stp.STAPLE_NORM_LAYER, rows, D, s_in, y0, weight=w,
+                        mean=mean, rstd=rstd)
+    nwb = stp.staple_norm_workspace_bytes(rows, D)
+    nws = torch.zeros(nwb, dtype=torch.uint8, device="cuda")
+    dw, db = (torch.empty(D, device="cuda") for _ in range(2))
+    dx = torch.empty_like(dy)
+    bf_y = torch.empty((T, D), dtype=torch.bfloat16, device="cuda")
+
+    def bf16(st):
+        stp.staple_ffn_fwd(ctx, stp.STAPLE_BF16, T, D, F, m.x, embeds[1], wg, wu, wd, z, bf_y, None,
+                           None, ws, wsb, stream=st)
+
+    def norm(st):
+        stp.staple_norm_bwd(ctx, stp.STAPLE_BF16, stp.STAPLE_NORM_LAYER, rows, D, dy, s_in, rstd,
+                            dx, mean=mean, weight=w, dw=dw, db=db, workspace=nws,
+                            workspace_bytes=nwb, stream=st)
+
+    jobs = [(lambda st, m=m, e=e: m.run(e, stream=st), m.y) for m, e in zip(layers, embeds)]
+    jobs += [(bf16, bf_y), (norm, dx)]
+    want = []
+    for run, out in jobs:
+        run(None)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        for _, out in jobs:
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _ in range(8):
+            for (run, _), st in zip(jobs, streams):
+                run(st)
+        torch.cuda.synchronize()
+        for (_, out), w0 in zip(jobs, want):
+            assert torch.equal(out, w0)
+    assert stp.staple_get_error(ctx) == 0
+
+
 def test_train_stack_as_a_residual_stream(stp, ctx):
     import torch
 
