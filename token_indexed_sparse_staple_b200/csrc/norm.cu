@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
   F2 s1 = f2(0.0f);
   constexpr int B = NV < 2 ? 1 : 2;      // (more at a time would not fit the registers)
   uint4 u[B];
+  const int draws = L == VEC ? t : stride_group(t, p.tpr);
   DropKey key{};
   if (DROP) key = drop_key(p.drop);
 #pragma unroll
@@ -89,8 +90,10 @@ __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdPa
 #pragma unroll
     for (int j = 0; j < 8; ++j) e[j] = xr[i].get(j);
     if (DROP && i % B == 0)
-      philox_n<B>(key, uint64_t(row) * uint64_t(G) + (t + i * p.tpr), uint32_t(p.tpr), u);
-    if (DROP) drop8(u[i % B], p.drop.below, p.drop.scale, e);
+      philox_n<B>(key, uint64_t(row) * uint64_t(G) + (draws + i * p.tpr), uint32_t(p.tpr), u);
+    if (DROP && L == VEC) drop8(u[i % B], p.drop.below, p.drop.scale, e);
+    if (DROP && L == STRIDE)
+      drop8_kept(stride_keep(u[i % B], p.drop.below, t, p.tpr), p.drop.scale, e);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[i][j] = f2(e[2 * j], e[2 * j + 1]);
     if (p.sum) {
@@ -202,6 +205,7 @@ __global__ void __launch_bounds__(512, NV == 1 && R == 1 ? 2 : 1)
     for (int j = 0; j < 8; ++j) aw[i][j] = ab[i][j] = 0.0f;
   wait_prior_kernels();
   if (p.part) release_dependents();
+  const int draws = L == VEC ? t : stride_group(t, p.tpr);
   DropKey key{};
   if (DROP) key = drop_key(p.drop);
   int buf = 0;
@@ -250,7 +254,16 @@ __global__ void __launch_bounds__(512, NV == 1 && R == 1 ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const Span e = span<L>(i, t, p.tpr, p.D);
-      if (e.n <= 0) break;
+      uint32_t keep[R];
+      if constexpr (DROP && L == STRIDE) {
+        // (by every lane, whatever it has of the row)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int64_t n = (r0 + rg * R + r) * G + (draws + i * p.tpr);
+          keep[r] = p.dx ? stride_keep(philox(key, uint64_t(n)), p.drop.below, t, p.tpr) : 0u;
+        }
+      }
+      if (e.n <= 0) continue;
       Raw8<BF16> w = ones_raw8<BF16>();
       if (p.w) w = load_raw8<BF16, L>(p.w, 0, e);
 #pragma unroll
@@ -274,7 +287,9 @@ __global__ void __launch_bounds__(512, NV == 1 && R == 1 ? 2 : 1)
         if (p.dsum) store_raw8<BF16, L>(p.dsum, row * p.D, e, pack_raw8<BF16>(d));
         if (p.dx) {
           // from the fp32 gradient, not from the rounded dsum
-          if (DROP)
+          if constexpr (DROP && L == STRIDE)
+            drop8_kept(keep[r], p.drop.scale, d);
+          else if (DROP)
             drop8(philox(key, uint64_t(row) * uint64_t(G) + (t + i * p.tpr)), p.drop.below,
                   p.drop.scale, d);
           store_raw8<BF16, L>(p.dx, row * p.D, e, pack_raw8<BF16>(d));
@@ -636,7 +651,7 @@ template <bool BF16, int NV>
 staple_status fwd_go(const FwdParams& p, bool vec, int grid, int block, cudaStream_t st) {
   void (*kern)(FwdParams);
   if (p.drop.rng)
-    kern = vec ? norm_fwd_kernel<BF16, NV, VEC, true> : norm_fwd_kernel<BF16, NV, GROUP, true>;
+    kern = vec ? norm_fwd_kernel<BF16, NV, VEC, true> : norm_fwd_kernel<BF16, NV, STRIDE, true>;
   else
     kern = vec ? norm_fwd_kernel<BF16, NV, VEC, false> : norm_fwd_kernel<BF16, NV, STRIDE, false>;
   cudaError_t ce = cudaSuccess;
@@ -663,7 +678,7 @@ constexpr int rows_in_flight(bool bf16, int nv) {
 template <bool BF16, int NV, int R>
 staple_status bwd_go(const BwdParams& p, bool vec, int grid, int block, size_t smem,
                      cudaStream_t st) {
-  void (*kern)(BwdParams) = p.drop.rng ? norm_bwd_kernel<BF16, NV, R, GROUP, true>
+  void (*kern)(BwdParams) = p.drop.rng ? norm_bwd_kernel<BF16, NV, R, STRIDE, true>
                                        : norm_bwd_kernel<BF16, NV, R, STRIDE, false>;
   // whole vectors come here only from rows too short for the ring kernel, and
   // from fp32 rows too long for it
@@ -771,21 +786,27 @@ struct DropoutParams {
   void* out;
   DropParams drop;
   int64_t units;
-  int32_t D, G;
+  int32_t D, G, tpr, per_row;
 };
 
 template <bool BF16, RowLayout L, bool DROP>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams p) {
   wait_prior_kernels();
+  // VEC: a unit is eight elements.  STRIDE: a row has `per_row` units, tpr of them
+  // (a warp's lanes, or fewer for short rows) side by side.
   const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (u >= p.units) return;
-  int64_t off = u * kGroup;
+  if (L == VEC && u >= p.units) return;
+  int64_t off = u * kGroup, draw = u;
   Span s{0, 1, kGroup};
-  if (L != VEC) {
-    const int64_t row = u / p.G;
-    const int e = int(u - row * p.G) * kGroup;
-    off = row * p.D + e;
-    s.n = min(kGroup, p.D - e);
+  const int t = L == VEC ? 0 : threadIdx.x & (p.tpr - 1);
+  if (L == STRIDE) {
+    const int64_t row = u / p.per_row;
+    const int g = int(u - row * p.per_row);
+    s.off = (g - t) * kGroup + t;
+    s.step = p.tpr;
+    s.n = u < p.units && s.off < p.D ? min(kGroup, (p.D - s.off + p.tpr - 1) / p.tpr) : 0;
+    off = row * p.D;
+    draw = row * p.G + g;
   }
   const Raw8<BF16> xr = load_raw8<BF16, L>(p.x, off, s);
   Raw8<BF16> rr = zero_raw8<BF16>();
@@ -793,7 +814,11 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams p) {
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = xr.get(j);
-  if (DROP) drop8(philox(drop_key(p.drop), uint64_t(u)), p.drop.below, p.drop.scale, v);
+  if (DROP) {
+    const uint4 draws = philox(drop_key(p.drop), uint64_t(draw));
+    if constexpr (L == VEC) drop8(draws, p.drop.below, p.drop.scale, v);
+    else drop8_kept(stride_keep(draws, p.drop.below, t, p.tpr), p.drop.scale, v);
+  }
   if (p.res)
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += rr.get(j);
@@ -883,11 +908,13 @@ staple_status launch_norm_bwd(const DeviceInfo& di, bool bf16, bool rms, int T, 
 staple_status launch_dropout(bool bf16, int T, int D, const void* x, const void* res,
                              const staple_drop* drop, void* out, cudaStream_t st) {
   if (T == 0) return STAPLE_OK;
-  DropoutParams p{x, res, out, drop_params(drop), 0, D, groups_of(D)};
-  p.units = int64_t(T) * p.G;
+  DropoutParams p{x, res, out, drop_params(drop), 0, D, groups_of(D), 0, 0};
   const bool vec = vec_ok(D, {x, res, out});
-  if (bf16) return vec ? dropout_go<true, VEC>(p, st) : dropout_go<true, GROUP>(p, st);
-  return vec ? dropout_go<false, VEC>(p, st) : dropout_go<false, GROUP>(p, st);
+  p.tpr = std::min(32, threads_per_row(p.G, 1));
+  p.per_row = vec ? p.G : (p.G + p.tpr - 1) / p.tpr * p.tpr;
+  p.units = int64_t(T) * p.per_row;
+  if (bf16) return vec ? dropout_go<true, VEC>(p, st) : dropout_go<true, STRIDE>(p, st);
+  return vec ? dropout_go<false, VEC>(p, st) : dropout_go<false, STRIDE>(p, st);
 }
 
 }  // namespace stp

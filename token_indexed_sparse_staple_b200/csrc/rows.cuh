@@ -21,11 +21,9 @@ struct Raw8 {
 };
 
 // How a thread's eight elements lie in a row.  VEC: side by side, on a 16-byte
-// boundary, all within the row.  GROUP: side by side, element by element.
-// STRIDE: one from each of eight runs of tpr elements, so that a warp's loads
-// are side by side; rows of an odd length take it unless dropout needs the
-// groups of eight that share a draw.
-enum RowLayout { VEC, GROUP, STRIDE };
+// boundary, all within the row.  STRIDE: one from each of eight runs of tpr
+// elements, so that a warp's loads are side by side, for rows of an odd length.
+enum RowLayout { VEC, STRIDE };
 
 // The elements of thread t's i-th eight: off + j * step for j < n, where n may
 // be zero or less.
@@ -62,7 +60,7 @@ __device__ __forceinline__ Raw8<BF16> load_raw8(const void* base, int64_t row, c
     }
   } else if constexpr (BF16) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + off;
-    const int step = L == GROUP ? 1 : s.step;
+    const int step = s.step;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t lo = 2 * i < s.n ? p[2 * i * step] : 0u;
@@ -71,7 +69,7 @@ __device__ __forceinline__ Raw8<BF16> load_raw8(const void* base, int64_t row, c
     }
   } else {
     const uint32_t* p = static_cast<const uint32_t*>(base) + off;
-    const int step = L == GROUP ? 1 : s.step;
+    const int step = s.step;
 #pragma unroll
     for (int i = 0; i < 8; ++i) r.w[i] = i < s.n ? p[i * step] : 0u;
   }
@@ -124,13 +122,13 @@ __device__ __forceinline__ void store_raw8(void* base, int64_t row, const Span& 
     }
   } else if constexpr (BF16) {
     uint16_t* p = static_cast<uint16_t*>(base) + off;
-    const int step = L == GROUP ? 1 : s.step;
+    const int step = s.step;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < s.n) p[i * step] = uint16_t((i & 1) ? r.w[i >> 1] >> 16 : r.w[i >> 1] & 0xffffu);
   } else {
     uint32_t* p = static_cast<uint32_t*>(base) + off;
-    const int step = L == GROUP ? 1 : s.step;
+    const int step = s.step;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < s.n) p[i * step] = r.w[i];
@@ -258,6 +256,42 @@ __device__ __forceinline__ void drop8(const uint4& u, uint32_t below, float scal
     const uint32_t draw = (i & 1) ? w[i >> 1] : w[i >> 1] << 16;
     v[i] = draw > below ? v[i] * scale : 0.0f;
   }
+}
+
+// Strided eights: the 8 * 32 elements of a warp's lanes (of a row's threads where
+// those are fewer) are as many whole groups, so each lane draws one group's eight,
+// in any order, and passes on a byte of which are kept.  (Whole groups per thread,
+// element by element, want no exchange but spread each of a warp's loads and
+// stores over 32 sectors: with dropout the norm of 16384 x 1023 fp32 took 122 us
+// forward and 133 backward, so 63 and 80; bf16 83 and 142, so 74 and 89.)  The
+// group that thread t draws, counted from the first of its i-th eights:
+__device__ __forceinline__ int stride_group(int t, int tpr) {
+  return tpr < 32 ? t : ((t & 31) >> 2) * (tpr >> 3) + ((t & ~31) >> 3) + (t & 3);
+}
+
+// ... and what thread t keeps of its eight, given its own draws; every lane of the
+// warp takes part.
+__device__ __forceinline__ uint32_t stride_keep(const uint4& u, uint32_t below, int t, int tpr) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t draw = (i & 1) ? w[i >> 1] : w[i >> 1] << 16;
+    mine |= draw > below ? 1u << i : 0u;
+  }
+  const int width = min(tpr, 32), at = t & (width - 1);
+  uint32_t keep = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int k = j * width + at;      // of the lanes' elements in order
+    keep |= (__shfl_sync(0xffffffffu, mine, k >> 3, width) >> (k & 7) & 1u) << j;
+  }
+  return keep;
+}
+
+__device__ __forceinline__ void drop8_kept(uint32_t keep, float scale, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = keep >> i & 1u ? v[i] * scale : 0.0f;
 }
 
 // ---------------------------------------------------------------------------
