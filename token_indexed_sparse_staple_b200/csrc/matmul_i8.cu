@@ -303,6 +303,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* box = s_out + q * kOutBox;
     float* scales = s_scale + q * BN;      // the tile's channel scales, a copy per warp
     int iter = 0;
+    // bf16 has two boxes, taken in turn from the first tile to the last: a tile at the
+    // right edge may end on either, and the wait below leaves the newest store in flight
+    int turn = 0;
     const uint32_t free_bar[2] = {map_peer(smem_u32(&tempty[0]), 0), map_peer(smem_u32(&tempty[1]), 0)};
     for (int t = first; t < ntiles; t += step, ++iter) {
       const int buf = iter & 1;
@@ -324,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < BN / 32; ++c) {
         const int n = nb * BN + c * 32;
         if (n >= p.N) break;          // the same for the whole warp
-        uint8_t* stg = box + (BF16 ? (c & 1) * (kOutBox / 2) : 0);
+        uint8_t* stg = box + (BF16 ? turn * (kOutBox / 2) : 0);
+        turn ^= 1;
         uint32_t r[32];
         tmem_ld32(tacc + c * 32, r);
         tmem_ld_wait(r);
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // stage the 32 x 32 block, swizzled as the TMA store expects it (and
         // free of bank conflicts either way)
         if (p.tma_out && lane == 0) {
-          // (bf16: the block before this one may still be on its way out)
+          // (bf16: the store from the other box may still be on its way out)
           if constexpr (BF16) bulk_wait_read1();
           else bulk_wait_read0();
         }
