@@ -804,7 +804,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams p) {
     const int g = int(u - row * p.per_row);
     s.off = (g - t) * kGroup + t;
     s.step = p.tpr;
-    s.n = u < p.units && s.off < p.D ? min(kGroup, (p.D - s.off + p.tpr - 1) / p.tpr) : 0;
+    // (not (D - off + tpr - 1) / tpr, which leaves 32 bits for D within tpr of 2^31)
+    s.n = u < p.units && s.off < p.D ? min(kGroup, (p.D - 1 - s.off) / p.tpr + 1) : 0;
     off = row * p.D;
     draw = row * p.G + g;
   }
