@@ -1,8 +1,11 @@
 """The operators around the layer at the far end of their sizes: rows of nearly 2^31
-elements.  Parts of them are checked against the fp64 definitions.
+elements, and tensors of more than 2^31, whose last rows lie behind offsets that 32
+bits do not hold.  Some rows of each are checked against the fp64 definitions.
 
 Tolerances, with u = 2^-24 and h = half a step of bf16 (2^-8): dropout rounds the
-scale and its product (3 u) and the sum (u) in fp32, then the output (h)."""
+scale and its product (3 u) and the sum (u) in fp32, then the output (h).  A sum over
+a row takes at most 32 adds per thread, 5 across a warp and 16 across warps, 53 u of
+the sum of the absolute values; 64 u covers it with the roundings of its terms."""
 from __future__ import annotations
 
 import numpy as np
@@ -95,3 +98,113 @@ def test_dropout_of_the_longest_rows(stp, ctx, D):
     kept = int((out != 0).sum())      # every element was written: a NaN counts as kept
     assert not bool(torch.isnan(out).any())
     assert abs(kept / D - (1 - p)) < 1e-4      # 10 standard deviations
+
+
+@pytest.mark.parametrize("D", [16384, 16383])
+@pytest.mark.parametrize("rms", [False, True])
+def test_norm_and_dropout_behind_two_to_the_31(stp, ctx, D, rms):
+    import torch
+    T, p, eps = 131200, 0.25, 1e-5
+    assert T * D > 2 ** 31 + D
+    rows = [0, 2 ** 31 // D - 1, 2 ** 31 // D, 2 ** 31 // D + 1, T - 1]
+    G = -(-D // 8)
+    f = np.stack([factors(t * G, D, p) for t in rows])
+    rng = rng_state()
+    drop = stp.make_drop(p, rng, SITE)
+    kind = stp.STAPLE_NORM_RMS if rms else stp.STAPLE_NORM_LAYER
+    BF = stp.STAPLE_BF16
+    x, res = random_bf16((T, D), 1), random_bf16((T, D), 2)
+    w = random_bf16(D, 3)
+    s, y = (torch.full_like(x, float("nan")) for _ in range(2))
+    mean, rstd = (torch.full((T,), float("nan"), device="cuda") for _ in range(2))
+    stp.staple_norm_fwd(ctx, BF, kind, T, D, x, y, weight=w, eps=eps, residual=res, drop=drop,
+                        sum=s, mean=mean, rstd=rstd)
+    xr, rr, sr, wr = np64(x[rows]), np64(res[rows]), np64(s[rows]), np64(w)
+    within(sr, rr + f * xr, H * np.abs(rr + f * xr) + 4 * U * (np.abs(f * xr) + np.abs(rr)), "sum")
+    want, mu, rs = bo.norm_fwd(sr, wr, None, eps, rms)
+    m1, c = np.abs(sr).mean(axis=1), np.abs(sr - mu[:, None])
+    dvar = 64 * U * ((c * c).mean(axis=1) + 2 * c.mean(axis=1) * m1 + eps)
+    within(np64(y[rows]), want, H * np.abs(want) + np.abs(wr) * rs[:, None] * 64 * U * m1[:, None]
+           + np.abs(want) * ((dvar * rs ** 2)[:, None] + 10 * U), "y")
+    # dropout by itself, over x's place
+    out = y
+    stp.staple_dropout(ctx, BF, T, D, x, drop, out, residual=res)
+    assert torch.equal(out, s)
+    del x, y, out
+    # backward: the gradient into res's place
+    dy, dsum_in = random_bf16((T, D), 4), res
+    dx = torch.full_like(dy, float("nan"))
+    dw, db = (torch.empty(D, device="cuda") for _ in range(2))
+    wsb = stp.staple_norm_workspace_bytes(T, D)
+    ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    ar = np64(dsum_in[rows])
+    stp.staple_norm_bwd(ctx, BF, kind, T, D, dy, s, rstd, dsum_in, mean=mean, weight=w,
+                        dsum_in=dsum_in, drop=drop, dx=dx, dw=dw, db=db, workspace=ws,
+                        workspace_bytes=wsb)
+    dyr, mu, rs = np64(dy[rows]), np64(mean[rows]), np64(rstd[rows])
+    ds = bo.norm_bwd(dyr, sr, mu, rs, wr, rms)[0] + ar
+    gw = np.abs(dyr * wr)
+    xh = np.abs((sr - (0.0 if rms else mu[:, None])) * rs[:, None])
+    tol = 64 * U * rs[:, None] * (gw + (0 if rms else gw.mean(axis=1, keepdims=True))
+                                  + xh * (gw * xh).mean(axis=1, keepdims=True))
+    tol += U * (np.abs(ar) + np.abs(ds))
+    within(np64(dsum_in[rows]), ds, H * np.abs(ds) + tol * (1 + H), "dsum")
+    within(np64(dx[rows]), f * ds, H * np.abs(f * ds) + f * (tol * (1 + H) + 3 * U * np.abs(ds)), "dx")
+    # dw and db over all rows: every row of a block's share is added in turn, and a block
+    # has at least T / 640 rows and at most all of T / 148 (148 blocks and more); then at
+    # most 20 blocks in each of 32 slices; xhat and its product round 4 times
+    n = -(-T // 148) + 20 + 32 + 4
+    for which, got in (("dw", dw), ("db", db)):
+        total, size = (torch.zeros(D, dtype=torch.float64, device="cuda") for _ in range(2))
+        for t in range(0, T, 4100):
+            v = dy[t:t + 4100].double()
+            if which == "dw":
+                m = 0.0 if rms else mean[t:t + 4100, None].double()
+                v *= (s[t:t + 4100].double() - m) * rstd[t:t + 4100, None].double()
+            total += v.sum(dim=0)
+            size += v.abs_().sum(dim=0)
+        within(np64(got), np64(total), n * U * np64(size), which)
+    assert stp.staple_get_error(ctx) == 0
+
+
+@pytest.mark.parametrize("D", [32768, 32761])
+def test_rows_to_8_bits_behind_two_to_the_31(stp, ctx, D):
+    import torch
+    T = 65700
+    assert T * D > 2 ** 31 + D
+    x = random_bf16((T, D), 1)
+    q = torch.full((T, D), 99, dtype=torch.int8, device="cuda")
+    scale = torch.full((T,), float("nan"), device="cuda")
+    stp.staple_quant_rows(ctx, stp.STAPLE_BF16, T, D, x, q, scale)
+    for t in (0, 2 ** 31 // D, 2 ** 31 // D + 1, T - 1):
+        wq, ws = bo.quant_rows(x[t:t + 1].float().cpu().numpy())
+        assert (q[t].cpu().numpy() == wq[0]).all() and float(scale[t]) == float(ws[0]), t
+
+
+def i8(shape, seed):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.empty(shape, dtype=torch.int8, device="cuda").random_(-128, 128, generator=g)
+
+
+# outputs (by TMA and by element), channels and tokens behind 2^31; each kernel
+@pytest.mark.parametrize("T, N, K", [(131200, 16400, 32), (131200, 16401, 32), (1, 17000, 131056),
+                                     (64, 17000, 131056), (300, 17000, 131056), (17000, 64, 131056),
+                                     (17000, 520, 131056)])
+def test_8_bit_product_behind_two_to_the_31(stp, ctx, T, N, K):
+    import torch
+    assert max(T * N, N * K, T * K) > 2 ** 31
+    a, b = i8((T, K), 1), i8((N, K), 2)
+    sa, sb = torch.rand(T, device="cuda") + 0.5, torch.rand(N, device="cuda") + 0.5
+    y = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    stp.staple_matmul_i8(ctx, stp.STAPLE_BF16, T, N, K, a, sa, b, sb, y)
+    rows, cols = (torch.cat([torch.arange(0, min(n, 40)), torch.arange(max(n - 40, 0), n)]).cuda()
+                  for n in (T, N))
+    # (integer sums below 2^31 are exact in fp64; rounded to fp32, multiplied twice, stored)
+    want = ((a[rows].double() @ b[cols].double().t()) * sa[rows].double()[:, None]
+            * sb[cols].double()[None, :])
+    got = y[rows][:, cols].double()
+    assert bool(((got - want).abs() <= (H + 4 * U) * want.abs()).all())
+    assert not bool(torch.isnan(y).any())
+    assert stp.staple_get_error(ctx) == 0
