@@ -1,0 +1,67 @@
+"""What the kernel in front of a call writes is what the call reads, although the call's
+kernel may start before that one has ended."""
+from __future__ import annotations
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def stp():
+    import token_indexed_sparse_staple_b200 as m
+    return m
+
+
+@pytest.fixture(scope="module")
+def ctx(stp):
+    c = stp.staple_context_create(0)
+    yield c
+    stp.staple_context_destroy(c)
+
+
+def replayed(calls, stream, graph):
+    """calls() on the stream, at once or through a captured graph."""
+    import torch
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                calls()
+            g.replay()
+        else:
+            calls()
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("T, N, K", [(1, 2048, 512), (40, 2048, 512), (40, 256, 8192),
+                                     (4096, 6144, 128)])
+def test_a_product_reads_scales_written_just_before_it(stp, ctx, T, N, K, graph):
+    """One token, the split kernel alone and in clusters, and tiles."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + N)
+    a, b = (torch.randint(-127, 128, (r, K), generator=g, device="cuda", dtype=torch.int8)
+            for r in (T, N))
+    kept = [[torch.rand(r, generator=g, device="cuda") + 0.1 for r in (T, N)] for _ in range(2)]
+    sa, sb = (torch.empty(r, device="cuda") for r in (T, N))
+    want, got = (torch.empty((n, T, N), dtype=torch.bfloat16, device="cuda") for n in (2, 10))
+
+    def call(i, out):
+        sa.copy_(kept[i][0])
+        sb.copy_(kept[i][1])
+        stp.staple_matmul_i8(ctx, stp.STAPLE_BF16, T, N, K, a, sa, b, sb, out)
+
+    for i in range(2):
+        call(i, want[i])
+        torch.cuda.synchronize()
+        ref = ((a.double() @ b.double().t()) * kept[i][0].double()[:, None]
+               * kept[i][1].double()[None, :])
+        tol = 2.0 ** -8 + 4 * 2.0 ** -24       # fp32 three times, then bf16
+        assert bool(((want[i].double() - ref).abs() <= tol * ref.abs()).all())
+    assert not torch.equal(*want)
+    replayed(lambda: [call(i % 2, got[i]) for i in range(10)], torch.cuda.Stream(), graph)
+    for i in range(10):
+        assert torch.equal(got[i], want[i % 2])

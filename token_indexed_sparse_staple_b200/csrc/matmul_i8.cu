@@ -133,6 +133,9 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N) {
 
 struct Params {
   int32_t T, N, K;
+  // The kernel in front may still be writing the scales when this one starts, so they
+  // are loaded after the wait and by ordinary loads: a read-only load (__ldg) is for
+  // what nothing writes while the kernel runs, and need not stay behind the wait.
   const float* a_scale;
   const float* b_scale;
   void* y;
@@ -312,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int mb, nb;
       tile_coords(t, p, mb, nb);
       const int m0 = mb * 2 * BM + rank * BM + q * 32, m = m0 + lane;
-      const float sa = m < p.T ? __ldg(p.a_scale + m) : 0.0f;
+      const float sa = m < p.T ? p.a_scale[m] : 0.0f;
 #pragma unroll
       for (int i = 0; i < BN / 32; ++i) {
         const int n = nb * BN + i * 32 + lane;
-        scales[i * 32 + lane] = n < p.N ? __ldg(p.b_scale + n) : 0.0f;
+        scales[i * 32 + lane] = n < p.N ? p.b_scale[n] : 0.0f;
       }
       __syncwarp();
       const bool ok = mbar_wait(&tfull[buf], uint32_t(iter >> 1) & 1, abort_flag, p.err, p.wait_ns);
@@ -530,15 +533,15 @@ __global__ void __launch_bounds__(kThreads)
   const int row = (warp & 3) * 32 + lane;   // this thread's accumulator row (warps 2..5)
   float sb[C == 1 ? 1 : 4];
   if constexpr (C == 1) {
-    sb[0] = row < channels ? __ldg(p.b_scale + n0 + row) : 0.0f;
+    sb[0] = row < channels ? p.b_scale[n0 + row] : 0.0f;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      sb[i] = lane * 4 + i < channels ? __ldg(p.b_scale + n0 + lane * 4 + i) : 0.0f;
+      sb[i] = lane * 4 + i < channels ? p.b_scale[n0 + lane * 4 + i] : 0.0f;
   }
   if (warp >= 2)
     for (int t = threadIdx.x - 64; t < tokens; t += kThreads - 64)
-      s_scale[t] = __ldg(p.a_scale + t0 + t);
+      s_scale[t] = p.a_scale[t0 + t];
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
