@@ -16,8 +16,8 @@ def code_of(name):
     return re.sub(r"//[^\n]*", "", text)
 
 
-@pytest.mark.parametrize("name", ["matmul_i8.cu"])
+@pytest.mark.parametrize("name", ["matmul_i8.cu", "norm.cu", "quant.cu", "rows.cuh"])
 def test_no_read_only_loads(name):
     code = code_of(name)
-    assert "wait_prior_kernels();" in code
+    assert name.endswith("h") or "wait_prior_kernels();" in code
     assert not re.findall(r"__ldg|\.global\.(?:\w+\.)*nc\b|__restrict__", code)

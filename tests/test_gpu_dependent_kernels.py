@@ -65,3 +65,38 @@ def test_a_product_reads_scales_written_just_before_it(stp, ctx, T, N, K, graph)
     replayed(lambda: [call(i % 2, got[i]) for i in range(10)], torch.cuda.Stream(), graph)
     for i in range(10):
         assert torch.equal(got[i], want[i % 2])
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("T, D", [(3, 64), (300, 2048), (300, 1001)])
+def test_dropout_reads_the_state_written_just_before_it(stp, ctx, T, D, graph):
+    """The norm forward and backward and dropout on its own, each behind an update of
+    {seed, offset} on the same stream: the masks are those of the updated state."""
+    import torch
+
+    from oracle import block_oracle as bo
+    p, n, seed, site = 0.5, 6, 1234567, 2
+    x = torch.rand((T, D), device="cuda") + 1.0          # dropped elements alone are zero
+    rng = torch.tensor([seed, 0], dtype=torch.int64, device="cuda")
+    drop = stp.make_drop(p, rng, site)
+    f32 = stp.STAPLE_F32
+    s, y, o, dx = (torch.empty((n, T, D), device="cuda") for _ in range(4))
+    rstd = torch.ones(T, device="cuda")
+    dsum_in = torch.full((T, D), 1e6, device="cuda")      # so that ds is nowhere zero
+
+    def calls():
+        rng[1] = 0
+        for i in range(n):
+            rng[1] += 1
+            stp.staple_norm_fwd(ctx, f32, stp.STAPLE_NORM_RMS, T, D, x, y[i], drop=drop, sum=s[i])
+            rng[1] += 1
+            stp.staple_dropout(ctx, f32, T, D, x, drop, o[i])
+            rng[1] += 1
+            stp.staple_norm_bwd(ctx, f32, stp.STAPLE_NORM_RMS, T, D, x, x, rstd, None,
+                                dsum_in=dsum_in, drop=drop, dx=dx[i])
+
+    replayed(calls, torch.cuda.Stream(), graph)
+    for i in range(n):
+        for k, got in enumerate((s[i], o[i], dx[i])):
+            keep = bo.dropout_factors(T, D, p, seed, 3 * i + k + 1, site) != 0
+            assert ((got != 0).cpu().numpy() == keep).all(), (i, k)
