@@ -85,7 +85,6 @@ def test_dropout_reads_the_state_written_just_before_it(stp, ctx, T, D, graph):
     dsum_in = torch.full((T, D), 1e6, device="cuda")      # so that ds is nowhere zero
 
     def calls():
-        rng[1] = 0
         for i in range(n):
             rng[1] += 1
             stp.staple_norm_fwd(ctx, f32, stp.STAPLE_NORM_RMS, T, D, x, y[i], drop=drop, sum=s[i])
