@@ -99,3 +99,34 @@ def test_dropout_reads_the_state_written_just_before_it(stp, ctx, T, D, graph):
         for k, got in enumerate((s[i], o[i], dx[i])):
             keep = bo.dropout_factors(T, D, p, seed, 3 * i + k + 1, site) != 0
             assert ((got != 0).cpu().numpy() == keep).all(), (i, k)
+
+
+def test_quantise_layer_on_another_stream(stp, ctx):
+    """The weights are written on the current stream, behind a wait, and so are the reads
+    of a tensor whose memory the copy then gets; the copy is read there afterwards."""
+    import torch
+
+    from token_indexed_sparse_staple_b200.stack import LayerWeights, quantise_layer
+    F, D = 512, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    src = [torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+           for s in ((F, D), (F, D), (D, F))]
+    want = quantise_layer(ctx, LayerWeights(*src))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        w = [torch.zeros_like(s) for s in src]
+        old = torch.full((2 * F, D), 5, dtype=torch.int8, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)        # about 10 ms
+        for a, b in zip(w, src):
+            a.copy_(b)
+        kept = old.clone()
+        del old
+        q = quantise_layer(ctx, LayerWeights(*w), stream=stream)
+        got = [t.clone() for t in (q.w_gate_up, q.gate_up_scale, q.w_down, q.down_scale)]
+        torch.cuda.synchronize()
+        assert (kept == 5).all()
+        for a, b in zip(got, (want.w_gate_up, want.gate_up_scale, want.w_down, want.down_scale)):
+            assert torch.equal(a, b)

@@ -61,15 +61,24 @@ class LayerWeightsI8:
 
 def quantise_layer(ctx, w: LayerWeights, stream=None) -> LayerWeightsI8:
     """The 8-bit copy of a layer's bf16 weights, made on `stream` (default:
-    torch's current stream)."""
+    torch's current stream).  With another stream, that one first waits for the
+    current stream, where the weights were made and the copy's memory is
+    allocated (memory that work still queued there may have used before), and the
+    current stream then waits for the copy."""
     import torch
+    current = torch.cuda.current_stream()
+    st = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream or current
     F, D = w.w_gate.shape
     gu = torch.empty((2 * F, D), dtype=torch.int8, device="cuda")
     gus = torch.empty(2 * F, dtype=torch.float32, device="cuda")
     down = torch.empty((D, F), dtype=torch.int8, device="cuda")
     ds = torch.empty(D, dtype=torch.float32, device="cuda")
+    if st != current:
+        st.wait_stream(current)
     for src, q, s in ((w.w_gate, gu[:F], gus[:F]), (w.w_up, gu[F:], gus[F:]), (w.w_down, down, ds)):
-        stp.staple_quant_rows(ctx, stp.STAPLE_BF16, *src.shape, src, q, s, stream=stream)
+        stp.staple_quant_rows(ctx, stp.STAPLE_BF16, *src.shape, src, q, s, stream=st)
+    if st != current:
+        current.wait_stream(st)
     return LayerWeightsI8(gu, gus, down, ds)
 
 
