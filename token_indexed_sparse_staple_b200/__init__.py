@@ -11,6 +11,7 @@ for any compute call.
 from __future__ import annotations
 
 import ctypes as C
+import operator
 
 import numpy as np
 
@@ -49,7 +50,8 @@ def _p(x) -> int | None:
     try:
         return x.data_ptr()     # tensors first: a call has up to ten of them
     except AttributeError:
-        return x.ctypes.data if isinstance(x, np.ndarray) else int(x)
+        # (an integer of another type is an address too; a float or a text is not)
+        return x.ctypes.data if isinstance(x, np.ndarray) else operator.index(x)
 
 
 def _current_stream() -> int:
