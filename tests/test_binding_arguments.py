@@ -8,6 +8,9 @@ import torch
 import token_indexed_sparse_staple_b200 as stp
 
 
+ORIGINAL = stp._current_stream      # before any call has chosen
+
+
 class Address(enum.IntEnum):
     A = 0x10000
 
@@ -28,3 +31,21 @@ def test_what_is_no_address_is_refused(v):
         stp._p(v)
     with pytest.raises(TypeError):
         stp.make_drop(0.1, v)
+
+
+class FakeStream:
+    cuda_stream = 4242
+
+
+@pytest.mark.parametrize("missing", [(), ("_cuda_getCurrentRawStream",), ("_cuda_getDevice",)])
+def test_the_current_stream_with_and_without_private_lookups(monkeypatch, missing):
+    monkeypatch.setattr(stp, "_current_stream", ORIGINAL)
+    monkeypatch.setattr(torch.cuda, "init", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: FakeStream)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
+    for name in missing:
+        monkeypatch.delattr(torch._C, name)
+    for _ in range(2):      # the first call chooses, later ones use its choice
+        assert stp._stream(None) == (4242 if missing else 1003)
+    assert stp._stream(7) == 7 and stp._stream(FakeStream) == 4242

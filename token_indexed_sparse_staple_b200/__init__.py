@@ -56,12 +56,17 @@ def _p(x) -> int | None:
 
 def _current_stream() -> int:
     """torch's current stream as a handle.  (torch.cuda.current_stream() builds
-    a Stream object, 3 us a call; these two lookups take 0.2.)"""
+    a Stream object, 3 us a call; torch's own two lookups behind it take 0.2.
+    They are private, so a torch without them gets the public call.)"""
     global _current_stream
     import torch
     torch.cuda.init()
-    device, handle = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    _current_stream = lambda: handle(device())
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if device and handle:
+        _current_stream = lambda: handle(device())
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream
     return _current_stream()
 
 
