@@ -33,24 +33,6 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
-// Wait until the kernels before this one in the stream have completed and
-// their writes are visible.  A kernel launched as a programmatic dependent may
-// start while the one before it drains; everything it reads from memory, and
-// everything it writes, comes after this.
-__device__ __forceinline__ void wait_prior_kernels() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-// Let the next kernel of the stream start, if it was launched as a programmatic
-// dependent, as soon as every block of this one has come this far.  Only where
-// that kernel is the library's own and part of the same call: another one
-// might read before it waits (the decode kernel fetches its weights so), and
-// what it reads might be this kernel's output.  After wait_prior_kernels(), so
-// that what it does read early is older than both.
-__device__ __forceinline__ void release_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // ---------------------------------------------------------------------------
 // bf16 <-> fp32
 // ---------------------------------------------------------------------------
@@ -197,10 +179,6 @@ __device__ __forceinline__ void bulk_commit() {
 // memory (the buffers may be written again).
 __device__ __forceinline__ void bulk_wait_read0() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-// The same for all but the last committed group.
-__device__ __forceinline__ void bulk_wait_read1() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 // Wait until this thread's committed bulk stores have completed.
 __device__ __forceinline__ void bulk_wait0() {

@@ -45,8 +45,9 @@ struct TraceScope {                                   // makes a tracer current 
 
 // Launch a kernel as a programmatic dependent of what is before it in the
 // stream: its blocks start, and set up what needs no memory, while the kernel
-// before drains.  The kernel calls wait_prior_kernels() before it touches
-// memory.  cluster: blocks per cluster along x.
+// before drains.  The kernel calls wait_prior_kernels() before it writes memory or
+// reads what a kernel before it may write (dependent.cuh has the rule).  cluster:
+// blocks per cluster along x.
 template <typename... P, typename... A>
 inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned block, size_t smem,
                                     cudaStream_t st, unsigned cluster, const A&... args) {

@@ -29,6 +29,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "internal.h"
 #include "tmap.h"
 
@@ -129,6 +130,11 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N) {
          | (1u << 10)                   // B format: s8
          | (uint32_t(N >> 3) << 17)     // N / 8
          | (uint32_t(M >> 4) << 24);    // M / 16
+}
+
+// bulk_wait_read0() for all but the last committed group.
+__device__ __forceinline__ void bulk_wait_read1() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 
 struct Params {

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "dependent.cuh"
 
 namespace stp {
 
