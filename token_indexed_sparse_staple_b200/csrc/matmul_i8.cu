@@ -182,9 +182,10 @@ __device__ __forceinline__ void tile_coords(int t, const Params& p, int& mb, int
   nb = r / rows;
 }
 
-// 16384 x 8192 x 2048 takes 170 us alone (3.23 P op/s, 0.94 of twice the
-// measured bf16 rate) and 209 back to back, where the 1 kW cap holds the clock
-// near 1.6 GHz; 128 x 256 tiles on single SMs took 189 and 229.
+// 16384 x 8192 x 2048 takes 165 us in captured runs with pauses between them (3.33 P
+// op/s, 0.97 of twice the measured bf16 rate) and 205 to 211 back to back, where the 1
+// kW cap holds the clock near 1.6 GHz; 128 x 256 tiles on single SMs took 189 and 229
+// when these took 170 and 209.  With fp32 outputs a captured run takes 210 us.
 //
 // Blocks 2i and 2i + 1 are a pair; the even one leads: it waits for both
 // blocks' loads and issues the products.
@@ -416,8 +417,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the rows that no copy wrote is not read), and the height is chosen so that
 // the tiles are as many as the SMs.  Only outputs too narrow for that, or with
 // so many tokens that their re-reading from L2 would cost more, split k too.
-// 64 x 11008 x 4096 takes 11.0 us a call among others (45 MB of weights in 6.5
-// of them), 64 x 8192 x 2048 7.9 in a captured run.
+// 64 x 11008 x 4096 takes 12.0 us in a captured run over weights enough that they come
+// from memory (45.1 MB, 7.0 us at a copy's rate), 9.6 where one or two sets of them
+// stay in L2; 64 x 8192 x 2048 takes 7.8 from memory.
 constexpr int kUnit = 2 * BK;               // 256 bytes of each row per stage
 constexpr int kMaxTokens = 256, kMaxStages = 24;
 
@@ -676,8 +678,8 @@ __global__ void __launch_bounds__(kThreads)
 // maps, barriers or tensor memory, whose 1.5 us before the first load the split
 // kernel has no work to hide behind here.  ksplit warps of a block share a pair
 // of channels where there are too few channels to keep HBM busy.  In a captured
-// run, beside two tokens in the split kernel: 8192 x 2048 4.8 us (6.7), 2048 x
-// 8192 4.5 (7.6), 11008 x 4096 9.3 (11.1).  Given two tokens the two kernels were
+// run, beside two tokens in the split kernel: 8192 x 2048 4.4 us (6.4), 2048 x
+// 8192 4.4 (7.1), 11008 x 4096 9.7 (10.8).  Given two tokens the two kernels were
 // even, given four the split kernel won.
 constexpr int kDotThreads = 256, kDotWarps = kDotThreads / 32, kDotRows = 2;
 constexpr int kDotChunks = 4;              // chunks of 512 bytes in flight per row

@@ -42,10 +42,10 @@ struct FwdParams {
 };
 
 // Forward.  One read of x and the residual, one write of the sum and y; a block
-// holds whole rows.  16384 x 2048 bf16 with residual takes 44.4 us without
-// dropout (6.05 TB/s, 0.94 of a copy) and 47.5 with it (0.88: the generator's
-// integer products share the issue slots), 1 x 4096 takes 3.6 us, 1537 x 1023
-// fp32 7.7 (captured runs).
+// holds whole rows.  In captured runs 16384 x 2048 bf16 with residual takes 44.0 us
+// without dropout (6.1 TB/s, 0.94 of a copy) and 47 to 49 with it (0.85 to 0.88: the
+// generator's integer products share the issue slots), 1 x 4096 2.7 us, 1537 x 1023
+// fp32 7.4 from memory and 5.9 from L2.
 template <bool BF16, int NV, RowLayout L, bool DROP>
 // (bf16: 64 registers, so that 32 warps share an SM)
 __global__ void __launch_bounds__(512, BF16 ? 2 : 1) norm_fwd_kernel(const FwdParams p) {
@@ -345,11 +345,11 @@ __global__ void __launch_bounds__(512, NV == 1 && R == 1 ? 2 : 1)
 // The stage that a group refills after the barrier of row i is the one of row
 // i - 1: by then every thread of the group has left row i - 1 behind.
 //
-// 16384 x 2048 bf16 with residual takes 77.8 us with dropout (335.9 MB, 4.3
-// TB/s) and 57.3 without (4.7 TB/s), dw and db included: bound by issue and the
-// latency of a row's chain at 16 warps per SM (58 % of the issue slots, 45
-// instructions per element, 17 of them dropout's).  The plain kernel above took
-// 117 us.
+// 16384 x 2048 bf16 with residual takes 77 to 81 us with dropout (335.9 MB, 4.2 to
+// 4.3 TB/s) and 59 to 62 without (268.8 MB, 4.3 to 4.5 TB/s) in captured runs, dw and
+// db included: bound by issue and the latency of a row's chain at 16 warps per SM
+// (with dropout 56 % of the issue slots, 43 instructions per element against 29
+// without).  The plain kernel above took 117 us.
 //
 // NV groups of eight per thread and row.  With two, what both passes use (gw
 // and xhat) stays in registers beside the 32 partial sums of dw and db; with
@@ -777,8 +777,9 @@ DropParams drop_params(const staple_drop* d) {
 }
 
 // Dropout with an optional residual on its own: unit n is group g of row t.
-// Bound by HBM: 8192 x 4096 bf16 with residual takes 33.5 us (6.0 TB/s, 0.93 of
-// a copy); the ten rounds per eight elements fit beside it.
+// Bound by HBM: 8192 x 4096 bf16 with residual takes 33.5 us a call among others (6.0
+// TB/s, 0.93 of a copy), 32 in a captured run; the ten rounds per eight elements fit
+// beside it.
 // VEC: D % 8 == 0, so n alone gives the address.
 struct DropoutParams {
   const void* x;
